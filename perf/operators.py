@@ -378,18 +378,22 @@ def _verify(s):
         q = s["draft"][here].double() if s["draft"] is not None else torch.zeros(seqs, vocab, dtype=torch.float64, device=DEV).scatter_(1, token[:, None], 1.0)
         taken = tried & (s["ua"][row].double() * q[each, token] * total < left[each, token])
         no = tried & ~taken
-        rest = (left / total[:, None] - q).clamp(min=0.0) if s["draft"] is not None else left.scatter(1, token[:, None], 0.0)
-        mass = rest.sum(1) if s["draft"] is not None else total - left[each, token]
-        no_more = no & (rest.sum(1) > 0)            # where nothing is left the old residual stays
-        left = torch.where(no_more[:, None], rest, left)
-        total = torch.where(no_more, mass, total)
+        if s["draft"] is not None:
+            rest = torch.where(total[:, None] > 0, (left / total[:, None] - q).clamp(min=0.0), 0.0)
+            mass = rest.sum(1)
+        else:
+            rest = left.scatter(1, token[:, None], 0.0)
+            mass = (total - left[each, token]).clamp(min=0.0)
+        left = torch.where(no[:, None], rest, left)
+        total = torch.where(no, mass, total)
         s["out"][each[taken], length[taken] - 1] = token[taken].int()
         s["path"][each[taken], length[taken]] = i
         length = length + taken
         cur = torch.where(taken, torch.full_like(cur, i), cur)
         left = torch.where(taken[:, None], s["target"][row].double(), left)
         total = torch.where(taken, torch.ones_like(total), total)
-    sums = left.cumsum(1)
+    # where nothing is left: the target's own row
+    sums = torch.where(left.sum(1, keepdim=True) > 0, left, s["target"][start[:-1] + cur].double()).cumsum(1)
     last = torch.searchsorted(sums, (s["us"].double() * sums[:, -1])[:, None], right=True)[:, 0].clamp(max=vocab - 1)
     s["out"][each, length - 1] = last.int()
     s["len"].copy_(length)
@@ -554,14 +558,14 @@ def _exact_verify(s):
                     at, more = r, True
                     break
                 if q is not None:
-                    rest = torch.clamp(p / mass - q, min=0)
-                    if float(rest.sum()) > 0:
-                        p, mass = rest, float(rest.sum())
+                    p = torch.clamp(p / mass - q, min=0) if mass > 0 else torch.zeros_like(p)
+                    mass = float(p.sum())
                 else:
-                    gone, rest = float(p[x]), p.clone()
-                    rest[x] = 0
-                    if float(rest.sum()) > 0:
-                        p, mass = rest, mass - gone
+                    mass = max(0.0, mass - float(p[x]))
+                    p = p.clone()
+                    p[x] = 0
+        if float(p.sum()) == 0:     # nothing left
+            p = s["target"][a + at].double()
         c = torch.cumsum(p, 0)
         said.append(min(int((c <= us[i] * float(c[-1])).sum()), len(c) - 1))
         out[i, :len(said)] = torch.tensor(said, dtype=torch.int32)
