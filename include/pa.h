@@ -81,6 +81,11 @@ typedef enum { PA_F32 = 0, PA_BF16 = 1, PA_FP8_E4M3 = 2 } pa_dtype;
                                      a sequence whose partition count differs from the
                                      one its items were planned with; pa_prefill_planned:
                                      an item naming a sequence outside the batch          */
+#define PA_DEVERR_POSITION 0x40u  /* pa_qk_norm_rope_append: position >= max_position     */
+#define PA_DEVERR_DRAFT 0x80u     /* drafted tokens: a parent that is not an earlier row, a
+                                     token outside the vocabulary, a probability row with
+                                     no finite mass, or a path that is not increasing within
+                                     its sequence's rows                                  */
 
 /* ------------------------------------------------------------------ cache writes */
 
@@ -548,6 +553,170 @@ int pa_prefill_planned(void* out, const void* q, const void* k_cache, const void
                        int block_size, int num_blocks, int max_blocks_per_seq,
                        int max_query_len, float scale, pa_dtype dtype, pa_stream_t stream);
 
+/* ------------------------------------------- decode steps with drafted tokens */
+/*
+ * A decode step that verifies drafted tokens handles several rows per sequence
+ * at once: its last accepted token and the tokens drafted after it, a chain or
+ * a tree. Per layer: pa_qk_norm_rope_append writes the rows' K and V behind the
+ * context, pa_decode_tree attends them; after the last layer pa_verify_draft
+ * decides what is kept, and per layer pa_kv_accept moves the kept rows into
+ * place; pa_bm_truncate gives the slots of the others back. The pages stop at
+ * one token per step ("What is paged attention in vLLM...", Step 4); these calls
+ * are this library's extension of the same block arithmetic.
+ *
+ * Rows. Sequence s's n rows are query_start[s] .. query_start[s+1] - 1 of the
+ * batch; row 0 is its last accepted token, rows 1 .. n - 1 drafted ones. Their K
+ * and V are the last n of its context_lens[s] = L cached tokens: row i is in
+ * cache position L - n + i, whatever its depth. parents (int32 [total_q]) names
+ * the row that each follows, within its sequence: an earlier row, or -1 for a
+ * row that follows the context alone. NULL: chains (row i follows row i - 1).
+ */
+
+/*
+ * pa_qk_norm_rope_append — the rows of one layer made ready in one pass: each
+ * query and key head normed and rotated, the keys and values written into their
+ * cache slots ("Paged Attention" (klaylearn.com glossary), definition: prefill
+ * and decode write K and V into blocks through the slot of each token). For a
+ * head's row x of token i, in float32:
+ *     y = x / sqrt(mean(x^2) + eps) * weight          (weight NULL: y = x)
+ *     (y_a, y_b) -> (y_a c - y_b s, y_b c + y_a s)    for each pair of the first
+ * rotary_dim elements, c and s the pair's cosine and sine at positions[i]; the
+ * rest of y as it is. One rounding at the end.
+ *
+ *   q_out, q       device, [num_tokens][num_heads][head_dim], rows of a head and
+ *                  heads of a token dense, tokens q_out_stride / q_stride elements
+ *                  apart (q, k and v may be parts of one packed projection). q_out
+ *                  may be q itself (with the same stride), else must not overlap
+ *                  q, k or v.
+ *   k, v           device, [num_tokens][num_kv_heads][head_dim], likewise.
+ *   positions      device, int32 [num_tokens]: rotation position. Negative: a
+ *                  padding row, nothing of it is read or written. >= max_position
+ *                  sets PA_DEVERR_POSITION and skips the token.
+ *   slot_mapping   device, int64 [num_tokens], as in pa_kv_append (distinct; a
+ *                  negative slot writes no K or V, q_out is still written).
+ *   cos_sin        device, float32 [max_position][rotary_dim]: a position's
+ *                  rotary_dim / 2 cosines, then its sines. 16-byte aligned.
+ *   rotary_dim     <= head_dim, a multiple of 16 (float32 rows: of 8).
+ *   interleaved    0: pair i is elements (i, i + rotary_dim / 2); else (2i, 2i + 1).
+ *   q_weight, k_weight  device, [head_dim] in the rows' type, or NULL: no norm.
+ *   k_cache, v_cache, k_scale, v_scale  as pa_kv_append (dtype PA_F32, PA_BF16) or
+ *                  pa_kv_append_fp8 (dtype PA_FP8_E4M3; bfloat16 rows, the float32
+ *                  result divided by its head's scale and rounded once to E4M3).
+ * Supported: head_dim 64 or 128. Strides a multiple of 16 bytes. Values are
+ * copied bit for bit (E4M3: quantised). num_tokens == 0 is a no-op.
+ */
+int pa_qk_norm_rope_append(void* q_out, const void* q, const void* k, const void* v,
+                           int64_t q_out_stride, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                           int num_tokens, const float* cos_sin, int max_position, int rotary_dim,
+                           int interleaved, const void* q_weight, const void* k_weight, float eps,
+                           void* k_cache, void* v_cache, const float* k_scale,
+                           const float* v_scale, int num_blocks, int block_size, int num_heads,
+                           int num_kv_heads, int head_dim, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * pa_decode_tree — attention of every row of the step: row i attends the L - n
+ * tokens before the step, itself and its ancestors:
+ *     out[row][j] = sum_t softmax_t(scale * q[row][j] . K_s[t][h]) V_s[t][h]
+ * over those t, K_s[t] read through block_tables[s] as in pa_decode, h = j /
+ * (num_heads / num_kv_heads). The rows' own K and V must already be in the cache.
+ *
+ *   out, q         device, bf16 [total_q][num_heads][head_dim]. Rows of total_q
+ *                  past the last sequence's are left as they are.
+ *   query_start    device, int32 [num_seqs + 1], non-decreasing; 0 <= n <=
+ *                  min(max_query_len, context_lens[s]) for every s, else
+ *                  PA_DEVERR_CONTEXT is set and that sequence is skipped (n = 0:
+ *                  no rows, nothing done).
+ *   parents        device, int32 [total_q] or NULL (above). A parent that is not
+ *                  an earlier row of the sequence or -1 sets PA_DEVERR_DRAFT and
+ *                  counts as -1.
+ *   max_query_len  host upper bound of n (<= total_q).
+ *   workspace      device, at least pa_decode_tree_workspace_bytes(...) bytes,
+ *                  contents on entry ignored; calls that share one must not
+ *                  overlap on the GPU. Does not depend on num_seqs or lengths.
+ * The work is cut over the GPU from the device's lengths, so a captured call may
+ * be replayed with other lengths (within max_query_len). The cuts depend on all
+ * lengths of the batch: a row's result is the same from call to call, and on any
+ * placement and block size, but its last bits may differ in another batch.
+ * Products in bf16 (tcgen05), softmax and sums in float32, softmax weights
+ * rounded to bf16. A V row that some row of the step sees must be finite.
+ * Supported: PA_BF16; head_dim 64 or 128; num_heads / num_kv_heads in {1, 2, 4,
+ * 8}; block_size a power of two in [8, 256]; scale > 0.
+ */
+size_t pa_decode_tree_workspace_bytes(int num_heads, int num_kv_heads, int head_dim,
+                                      int max_query_len);
+int pa_decode_tree(void* out, const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, const int32_t* context_lens,
+                   const int32_t* query_start, const int32_t* parents, int num_seqs, int total_q,
+                   int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks,
+                   int max_blocks_per_seq, int max_query_len, float scale, void* workspace,
+                   size_t workspace_bytes, pa_dtype dtype, pa_stream_t stream);
+
+/*
+ * pa_verify_draft — which drafted tokens the target accepts, and its next token,
+ * from given random numbers, so that the tokens are distributed as the target's
+ * own. Per sequence, from row 0 on: the children of the last accepted row are
+ * tried in order. With R = target_probs[row] and Z = 1 at first, child c with
+ * token x is accepted when
+ *     u_accept[c] * draft_probs[row][x] * Z < R[x],
+ * and the walk goes on from c. Otherwise R := max(R / Z - draft_probs[row], 0),
+ * Z := sum R, and the next child is tried. When none is left, the last token is
+ * the lowest index whose running sum of R exceeds u_sample[s] * sum R.
+ * draft_probs NULL: drafts that were picked, not sampled (their distribution is
+ * 1 at the token): x is accepted when u_accept[c] * Z < R[x], else R[x] := 0 and
+ * Z is lessened by it. Where a rejection leaves no mass, later children are
+ * rejected and the last token is drawn from target_probs[row] itself.
+ *
+ *   out_tokens     device, int32 [num_seqs][max_query_len]: the accepted drafted
+ *                  tokens, then the last one; the rest -1.
+ *   out_path       device, int32 [num_seqs][max_query_len]: the rows kept: 0, then
+ *                  the accepted ones (increasing); the rest -1.
+ *   out_len        device, int32 [num_seqs]: tokens in out_tokens = rows in
+ *                  out_path (0 for a sequence without rows).
+ *   target_probs   device, float32, row r at r * target_stride: the target's
+ *                  probabilities of the token after row r, [vocab_size]. Rows are
+ *                  taken to sum to 1; values not > 0 count as 0.
+ *   draft_probs    device, float32, likewise with draft_stride: what row r's
+ *                  children were sampled from (leaves: not read); or NULL.
+ *   draft_tokens   device, int32 [total_q]: each row's token (row 0: not read).
+ *   parents, query_start  as above, n <= max_query_len; a bad range sets
+ *                  PA_DEVERR_CONTEXT and gives out_len 0. A parent that is not an
+ *                  earlier row, or a token outside the vocabulary, sets
+ *                  PA_DEVERR_DRAFT and the row is not tried.
+ *   u_accept       device, float32 [total_q], u_sample float32 [num_seqs]:
+ *                  uniform in [0, 1).
+ * Sums and comparisons are in float64. A final row without finite mass sets
+ * PA_DEVERR_DRAFT and gives token -1. max_query_len <= 1024.
+ */
+int pa_verify_draft(int32_t* out_tokens, int32_t* out_path, int32_t* out_len,
+                    const float* target_probs, int64_t target_stride, const float* draft_probs,
+                    int64_t draft_stride, const int32_t* draft_tokens, const int32_t* parents,
+                    const int32_t* query_start, const float* u_accept, const float* u_sample,
+                    int num_seqs, int total_q, int vocab_size, int max_query_len,
+                    pa_stream_t stream);
+
+/*
+ * pa_kv_accept — move the cache rows that verification kept into place: for each
+ * sequence, with base = context_lens[s] - n, the K and V rows of position base +
+ * path[s][j] go to position base + j, for j < path_len[s] (all reads as before
+ * the call). The context is then base + path_len[s] tokens (pa_bm_truncate).
+ *
+ *   path           device, int32 [num_seqs][max_path_len], increasing rows of the
+ *                  step, as pa_verify_draft's out_path.
+ *   path_len       device, int32 [num_seqs], in [0, min(n, max_path_len)].
+ *   context_lens, query_start  as the step's pa_decode_tree.
+ * Blocks that hold the step's rows must not be shared. A bad range sets
+ * PA_DEVERR_CONTEXT, a bad path or length PA_DEVERR_DRAFT (the sequence is
+ * skipped from its 32-entry stretch of the path on), a table entry outside the
+ * pool PA_DEVERR_BLOCK_ID (that row is skipped). Any dtype; block_size a power
+ * of two; rows of num_kv_heads * head_dim elements, a multiple of 16 bytes.
+ */
+int pa_kv_accept(void* k_cache, void* v_cache, const int32_t* block_tables,
+                 const int32_t* context_lens, const int32_t* query_start, const int32_t* path,
+                 const int32_t* path_len, int num_seqs, int max_path_len, int num_blocks,
+                 int block_size, int max_blocks_per_seq, int num_kv_heads, int head_dim,
+                 pa_dtype dtype, pa_stream_t stream);
+
 /*
  * pa_decode_noalloc — pa_decode for callers that cannot allocate device memory.
  * The pages have no counterpart: this is an interface convenience of this
@@ -685,6 +854,14 @@ int pa_bm_append_slots(pa_bm* bm, const int32_t* seq_ids, const int32_t* counts,
  */
 int pa_bm_block_tables(const pa_bm* bm, const int32_t* seq_ids, int n, int32_t* tables,
                        int max_blocks_per_seq, int32_t* context_lens);
+
+/*
+ * pa_bm_truncate — drop the sequence's tokens past new_len (rejected drafts):
+ * blocks that hold none of the remaining tokens lose this sequence's reference,
+ * last first. PA_ERR_INVALID for an unknown id or new_len outside [0, length];
+ * nothing changes then.
+ */
+int pa_bm_truncate(pa_bm* bm, int32_t seq_id, int32_t new_len);
 
 #ifdef __cplusplus
 }

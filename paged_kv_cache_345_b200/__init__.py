@@ -21,6 +21,14 @@ Entry points (same names as the C ABI):
   pa_prefill_plan, pa_prefill_planned
                    host work list of the prefill's items in the kernel's
                    longest-first order, and the prefill on it
+  pa_qk_norm_rope_append
+                   query and key heads normed and rotated, K and V written to
+                   their slots, in one pass
+  pa_decode_tree   attention of several drafted tokens per sequence (a chain or
+                   a tree) over the paged context
+  pa_verify_draft  accept drafted tokens and draw the next one, from given
+                   random numbers
+  pa_kv_accept     move the accepted rows' K and V into place
   BlockManager     host free list + reference counts + block tables
 """
 
@@ -44,6 +52,8 @@ __all__ = [
     "pa_set_decode_options", "PA_DECODE_EARLY_CACHE_READS", "decode_options",
     "pa_decode_contiguous", "pa_decode_shared_prefix", "pa_decode_shared_prefix_workspace_bytes",
     "pa_decode_plan", "pa_decode_planned", "pa_prefill_plan", "pa_prefill_planned",
+    "pa_qk_norm_rope_append", "pa_decode_tree", "pa_decode_tree_workspace_bytes",
+    "pa_verify_draft", "pa_kv_accept", "PA_DEVERR_POSITION", "PA_DEVERR_DRAFT",
 ]
 
 PA_OK, PA_ERR_INVALID, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_NO_BLOCKS, PA_ERR_DEVICE_CHECK = \
@@ -52,6 +62,7 @@ PA_F32, PA_BF16, PA_FP8_E4M3 = 0, 1, 2
 PA_DEVERR_SLOT, PA_DEVERR_BLOCK_ID, PA_DEVERR_CONTEXT, PA_DEVERR_COPY_PAIR, PA_DEVERR_TIMEOUT = \
     0x1, 0x2, 0x4, 0x8, 0x10
 PA_DEVERR_PLAN = 0x20
+PA_DEVERR_POSITION, PA_DEVERR_DRAFT = 0x40, 0x80
 
 lib_path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa.so")
 if not os.path.exists(lib_path):
@@ -102,6 +113,15 @@ _sig("pa_prefill_planned", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _
      _i32, _i32, _i32, _i32, _i32, _i32, _f32, _i32, _vp)
 _sig("pa_prefill", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32,
      _i32, _i32, _f32, _i32, _vp)
+_sig("pa_qk_norm_rope_append", _i32, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _i64, _vp, _vp, _i32, _vp,
+     _i32, _i32, _i32, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp)
+_sig("pa_decode_tree_workspace_bytes", _sz, _i32, _i32, _i32, _i32)
+_sig("pa_decode_tree", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32,
+     _i32, _i32, _i32, _i32, _f32, _vp, _sz, _i32, _vp)
+_sig("pa_verify_draft", _i32, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _i32,
+     _i32, _i32, _i32, _vp)
+_sig("pa_kv_accept", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
+     _i32, _i32, _vp)
 _sig("pa_decode_noalloc", _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32,
      _i32, _i32, _f32, _i32, _i32, _vp)
 _sig("pa_decode_noalloc_scratch_bytes", _sz)
@@ -128,6 +148,7 @@ _sig("pa_bm_seq_len", _i32, _vp, ctypes.c_int32)
 _sig("pa_bm_seq_num_blocks", _i32, _vp, ctypes.c_int32)
 _sig("pa_bm_append_slots", _i32, _vp, _i32p, _i32p, _i32, _i64p, _i64p, _i32,
      ctypes.POINTER(ctypes.c_int))
+_sig("pa_bm_truncate", _i32, _vp, ctypes.c_int32, ctypes.c_int32)
 _sig("pa_bm_block_tables", _i32, _vp, _i32p, _i32, _i32p, _i32, _i32p)
 
 EXPORTED = (
@@ -137,6 +158,8 @@ EXPORTED = (
     "pa_decode_shared_prefix_workspace_bytes",
     "pa_decode_fp8", "pa_decode_append_fp8", "pa_decode_plan", "pa_decode_planned",
     "pa_prefill_plan", "pa_prefill_planned",
+    "pa_qk_norm_rope_append", "pa_decode_tree", "pa_decode_tree_workspace_bytes",
+    "pa_verify_draft", "pa_kv_accept", "pa_bm_truncate",
     "pa_prefill", "pa_decode_noalloc", "pa_decode_noalloc_scratch_bytes", "pa_device_errors",
     "pa_last_error", "pa_status_string", "pa_alloc_create",
     "pa_alloc_destroy", "pa_alloc_block", "pa_incref", "pa_decref", "pa_refcount", "pa_num_free",
@@ -659,6 +682,187 @@ def pa_prefill_plan(query_start, context_lens, num_heads: int, num_kv_heads: int
     return out[:n.value]
 
 
+def _dev_rows(t, name, heads, dtype):
+    """(pointer, elements between tokens) of a [N, heads, d] view whose heads are
+    dense: a contiguous tensor, or one part of a packed projection."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    n, h, d = t.shape
+    if h != heads or (t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name} must be [N, {heads}, head_dim] with dense heads")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else h * d)
+
+
+def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
+                           q_weight=None, k_weight=None, eps: float = 1e-6,
+                           interleaved: bool = False, k_scale=None, v_scale=None,
+                           stream=None) -> None:
+    """Norm (with q_weight / k_weight [d]) and rotate every query and key head, write
+    q to q_out and K and V to their cache slots, in one pass.
+
+    q_out, q: [N, Hq, d], k, v: [N, Hkv, d], tokens any 16-byte-aligned stride
+    apart (q_out may be q); positions: int32 [N]; slot_mapping: int64 [N];
+    cos_sin: float32 [max_position, rotary_dim], cosines then sines; k_scale,
+    v_scale: with E4M3 caches. See pa_qk_norm_rope_append in include/pa.h."""
+    torch = _torch()
+    nb, bs, hkv, d = k_cache.shape
+    fp8 = _is_fp8(k_cache)
+    dt = torch.bfloat16 if fp8 else k_cache.dtype
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != d or k.shape[2] != d or \
+            q_out.shape != q.shape or v.shape != k.shape or k.shape[0] != q.shape[0]:
+        raise ValueError("q/q_out must be [N, num_heads, head_dim], k/v [N, num_kv_heads, head_dim]")
+    n, hq = q.shape[:2]
+    if v_cache.shape != k_cache.shape or positions.shape != (n,) or slot_mapping.shape != (n,):
+        raise ValueError("cache, positions or slot_mapping shape mismatch")
+    if cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be [max_position, rotary_dim]")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.shape != (d,):
+            raise ValueError(f"{name} must be [head_dim]")
+    if fp8 != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale go with (and only with) E4M3 caches")
+    if fp8 and (k_scale.shape != (hkv,) or v_scale.shape != (hkv,)):
+        raise ValueError("k_scale/v_scale must be [num_kv_heads]")
+    opt = lambda t, nm, ty: None if t is None else _dev_ptr(t, nm, ty)  # noqa: E731
+    guard, st = _on_device((q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
+                            q_weight, k_weight, k_scale, v_scale), stream)
+    with guard:
+        (po, so), (pq, sq) = _dev_rows(q_out, "q_out", hq, dt), _dev_rows(q, "q", hq, dt)
+        (pk, sk), (pv, sv) = _dev_rows(k, "k", hkv, dt), _dev_rows(v, "v", hkv, dt)
+        _check(_lib.pa_qk_norm_rope_append(
+            po, pq, pk, pv, so, sq, sk, sv, _dev_ptr(positions, "positions", torch.int32),
+            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
+            _dev_ptr(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0], cos_sin.shape[1],
+            int(bool(interleaved)), opt(q_weight, "q_weight", dt), opt(k_weight, "k_weight", dt),
+            float(eps), _dev_ptr(k_cache, "k_cache"),
+            _dev_ptr(v_cache, "v_cache", None if fp8 and _is_fp8(v_cache) else k_cache.dtype),
+            opt(k_scale, "k_scale", torch.float32), opt(v_scale, "v_scale", torch.float32), nb, bs,
+            hq, hkv, d, _dtype_code(k_cache), st))
+
+
+def pa_decode_tree_workspace_bytes(num_heads, num_kv_heads, head_dim, max_query_len) -> int:
+    return int(_lib.pa_decode_tree_workspace_bytes(num_heads, num_kv_heads, head_dim,
+                                                   max_query_len))
+
+
+def pa_decode_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents,
+                   max_query_len: int, scale: float, workspace, stream=None) -> None:
+    """Attention of each sequence's last rows (drafted tokens: a tree by parents, or
+    chains with parents None) over its paged context, each row seeing what was
+    cached before the step, itself and its ancestors.
+
+    q, out: bf16 [total_q, Hq, d]; query_start: int32 [S + 1]; context_lens: int32
+    [S], the rows counted; parents: int32 [total_q] or None; workspace: a uint8
+    CUDA tensor of at least pa_decode_tree_workspace_bytes(...) bytes. See
+    pa_decode_tree in include/pa.h."""
+    torch = _torch()
+    nb, bs, hkv, d = k_cache.shape
+    total_q, hq, dq = q.shape
+    s = context_lens.shape[0]
+    if dq != d or out.shape != q.shape or v_cache.shape != k_cache.shape:
+        raise ValueError("q/out/cache shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != s or query_start.shape != (s + 1,):
+        raise ValueError("block_tables must be [S, max_blocks], query_start [S + 1]")
+    if parents is not None and parents.shape != (total_q,):
+        raise ValueError("parents must be [total_q]")
+    if workspace is None:
+        raise ValueError("pa_decode_tree needs a workspace")
+    dt = k_cache.dtype
+    guard, st = _on_device((out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                            parents, workspace), stream)
+    with guard:
+        _check(_lib.pa_decode_tree(
+            _dev_ptr(out, "out", dt), _dev_ptr(q, "q", dt), _dev_ptr(k_cache, "k_cache"),
+            _dev_ptr(v_cache, "v_cache", dt), _dev_ptr(block_tables, "block_tables", torch.int32),
+            _dev_ptr(context_lens, "context_lens", torch.int32),
+            _dev_ptr(query_start, "query_start", torch.int32),
+            None if parents is None else _dev_ptr(parents, "parents", torch.int32), s, total_q, hq,
+            hkv, d, bs, nb, block_tables.shape[1], int(max_query_len), float(scale),
+            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _dtype_code(k_cache), st))
+
+
+def _prob_rows(t, name, rows, vocab):
+    """(pointer, floats between rows) of a float32 [rows, vocab] tensor with dense rows."""
+    torch = _torch()
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if tuple(t.shape) != (rows, vocab) or (vocab > 1 and t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name} must be [total_q, vocab_size] with dense rows")
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if rows > 1 else vocab)
+
+
+def pa_verify_draft(out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens,
+                    parents, query_start, u_accept, u_sample, stream=None) -> None:
+    """Accept drafted tokens against the target's probabilities and draw each
+    sequence's next token, from given random numbers.
+
+    out_tokens, out_path: int32 [S, max_query_len], out_len: int32 [S];
+    target_probs, draft_probs (or None: picked drafts): float32 [total_q, V], any
+    row stride; draft_tokens, parents (or None: chains): int32 [total_q];
+    query_start: int32 [S + 1]; u_accept: float32 [total_q], u_sample: float32
+    [S]. See pa_verify_draft in include/pa.h."""
+    torch = _torch()
+    if out_tokens.dim() != 2 or out_path.shape != out_tokens.shape:
+        raise ValueError("out_tokens and out_path must be [S, max_query_len]")
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [total_q, vocab_size]")
+    s, most = out_tokens.shape
+    total_q, vocab = target_probs.shape
+    if out_len.shape != (s,) or query_start.shape != (s + 1,) or u_sample.shape != (s,):
+        raise ValueError("out_len and u_sample must be [S], query_start [S + 1]")
+    for t, name in ((draft_tokens, "draft_tokens"), (u_accept, "u_accept"), (parents, "parents")):
+        if t is not None and t.shape != (total_q,):
+            raise ValueError(f"{name} must be [total_q]")
+    i32, f32 = torch.int32, torch.float32
+    guard, st = _on_device((out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens,
+                            parents, query_start, u_accept, u_sample), stream)
+    with guard:
+        pt, ts = _prob_rows(target_probs, "target_probs", total_q, vocab)
+        pd, ds = (None, 0) if draft_probs is None else \
+            _prob_rows(draft_probs, "draft_probs", total_q, vocab)
+        _check(_lib.pa_verify_draft(
+            _dev_ptr(out_tokens, "out_tokens", i32), _dev_ptr(out_path, "out_path", i32),
+            _dev_ptr(out_len, "out_len", i32), pt, ts, pd, ds,
+            _dev_ptr(draft_tokens, "draft_tokens", i32),
+            None if parents is None else _dev_ptr(parents, "parents", i32),
+            _dev_ptr(query_start, "query_start", i32), _dev_ptr(u_accept, "u_accept", f32),
+            _dev_ptr(u_sample, "u_sample", f32), s, total_q, vocab, most, st))
+
+
+def pa_kv_accept(k_cache, v_cache, block_tables, context_lens, query_start, path, path_len,
+                 stream=None) -> None:
+    """Move each sequence's accepted rows into place: the K and V of its row
+    path[s, j] go to where its row j is, for j < path_len[s].
+
+    path: int32 [S, max_path_len], path_len: int32 [S] (pa_verify_draft's out_path
+    and out_len); the rest as in the step's pa_decode_tree. See pa_kv_accept in
+    include/pa.h."""
+    torch = _torch()
+    nb, bs, hkv, d = k_cache.shape
+    s = context_lens.shape[0]
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("cache shape mismatch")
+    if block_tables.dim() != 2 or block_tables.shape[0] != s or query_start.shape != (s + 1,):
+        raise ValueError("block_tables must be [S, max_blocks], query_start [S + 1]")
+    if path.dim() != 2 or path.shape[0] != s or path_len.shape != (s,):
+        raise ValueError("path must be [S, max_path_len], path_len [S]")
+    i32 = torch.int32
+    guard, st = _on_device((k_cache, v_cache, block_tables, context_lens, query_start, path,
+                            path_len), stream)
+    with guard:
+        _check(_lib.pa_kv_accept(
+            _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", k_cache.dtype),
+            _dev_ptr(block_tables, "block_tables", i32), _dev_ptr(context_lens, "context_lens", i32),
+            _dev_ptr(query_start, "query_start", i32), _dev_ptr(path, "path", i32),
+            _dev_ptr(path_len, "path_len", i32), s, path.shape[1], nb, bs, block_tables.shape[1],
+            hkv, d, _dtype_code(k_cache), st))
+
+
 def pa_device_errors(stream=None) -> int:
     """Synchronise, read and clear the device error word; returns its PA_DEVERR_* bits."""
     torch = _torch()
@@ -770,6 +974,10 @@ class BlockManager:
 
     def seq_num_blocks(self, seq: int) -> int:
         return int(_lib.pa_bm_seq_num_blocks(self._h, seq))
+
+    def truncate(self, seq: int, new_len: int) -> None:
+        """Drop the sequence's tokens past new_len; blocks left empty lose its reference."""
+        _check(_lib.pa_bm_truncate(self._h, seq, new_len))
 
     def append_slots(self, seq_ids, counts, slots_out=None, cows_out=None):
         """Reserve slots; returns (slot_mapping int64 [sum(counts)], cow_pairs int64 [k, 2]).

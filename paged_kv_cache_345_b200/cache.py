@@ -23,6 +23,15 @@ workspace. Each method marshals arguments and calls libpa.so:
       sequences' first n tokens (a multiple of the block size) sit in the same
       blocks (forked from one parent): pa_decode_shared_prefix attends them once
       for the batch, beside the decode of each sequence's own tokens; bf16.
+  A step that verifies drafted tokens (n rows per sequence: its last token, then
+  the drafted ones, a chain or a tree):
+  write_rows(q, k, v, seq_ids, counts, positions, cos_sin)  reserve the rows'
+      slots (shared tail blocks copied first), then norm, rotate and write them
+      in one pass (pa_qk_norm_rope_append); returns the queries.
+  decode_tree(q, seq_ids, counts, parents)  every row attends what was cached
+      before the step, itself and its ancestors (pa_decode_tree); bf16.
+  accept(seq_ids, counts, path, path_len)  after pa_verify_draft: move the kept
+      rows into place (pa_kv_accept) and give the others' slots back.
 
 dtype "fp8_e4m3": the caches hold uint8 E4M3 codes with one float32 scale per
 KV head (k_scale, v_scale); rows come in as bfloat16 and are quantised on the
@@ -44,8 +53,10 @@ import torch
 from . import (BlockManager, pa_copy_blocks, pa_decode, pa_decode_append, pa_decode_append_fp8,
                pa_decode_fp8, pa_decode_partition_size, pa_decode_plan, pa_decode_planned,
                pa_decode_shared_prefix,
-               pa_decode_shared_prefix_workspace_bytes, pa_decode_workspace_bytes, pa_kv_append,
-               pa_kv_append_fp8, pa_prefill, pa_prefill_plan)
+               pa_decode_shared_prefix_workspace_bytes, pa_decode_tree,
+               pa_decode_tree_workspace_bytes, pa_decode_workspace_bytes, pa_kv_accept,
+               pa_kv_append, pa_kv_append_fp8, pa_prefill, pa_prefill_plan,
+               pa_qk_norm_rope_append)
 
 _TORCH_DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16, "fp8_e4m3": torch.uint8}
 
@@ -256,3 +267,61 @@ class PagedKVCache:
                              context_lens, max_len, scale, partition_size, ws,
                              stream=self.stream)
         return out
+
+    # ----------------------------------------------- steps with drafted tokens
+    @_on_stream
+    def write_rows(self, q, k, v, seq_ids, counts, positions, cos_sin, q_weight=None,
+                   k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None):
+        """Append counts[i] rows to seq_ids[i] with their norms and rotation: q [N, Hq, d],
+        k, v [N, Hkv, d] (parts of one packed projection will do), positions int32 [N]
+        and cos_sin on the device; the rotated queries are returned."""
+        slots, cows = self.bm.append_slots(seq_ids, counts)
+        if len(cows):
+            pa_copy_blocks(self.k_cache, self.v_cache, self._to_device(cows), stream=self.stream)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        if len(slots):
+            sc = dict(k_scale=self.k_scale, v_scale=self.v_scale) if self.fp8 else {}
+            pa_qk_norm_rope_append(q_out, q, k, v, positions, self._to_device(slots), self.k_cache,
+                                   self.v_cache, cos_sin, q_weight, k_weight, eps, interleaved,
+                                   stream=self.stream, **sc)
+        return q_out
+
+    def _query_start(self, counts):
+        return np.concatenate([[0], np.cumsum(np.asarray(counts, dtype=np.int64))]).astype(np.int32)
+
+    @_on_stream
+    def decode_tree(self, q, seq_ids, counts, parents=None, scale: float | None = None, out=None):
+        """Attend each sequence's last counts[i] rows (already written): q [sum(counts), Hq,
+        d]; parents int32 [sum(counts)] on the device, or None for chains."""
+        if self.fp8:
+            raise NotImplementedError("pa_decode_tree reads bf16 caches")
+        out = torch.empty_like(q) if out is None else out
+        if not len(seq_ids) or not max(counts):
+            return out
+        block_tables, context_lens, _ = self.tables(seq_ids)
+        most = int(max(counts))
+        scale = 1.0 / float(np.sqrt(self.head_dim)) if scale is None else scale
+        need = pa_decode_tree_workspace_bytes(q.shape[1], self.num_kv_heads, self.head_dim, most)
+        if need > self._workspace.numel():
+            self._workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        pa_decode_tree(out, q, self.k_cache, self.v_cache, block_tables, context_lens,
+                       self._to_device(self._query_start(counts)), parents, most, scale,
+                       self._workspace, stream=self.stream)
+        return out
+
+    @_on_stream
+    def accept(self, seq_ids, counts, path, path_len):
+        """Keep the rows that pa_verify_draft kept (its out_path and out_len) of the step of
+        counts[i] rows per sequence; the others' slots go back. Returns the new context
+        lengths (waits for path_len)."""
+        if not len(seq_ids):
+            return []
+        block_tables, context_lens, _ = self.tables(seq_ids)
+        pa_kv_accept(self.k_cache, self.v_cache, block_tables, context_lens,
+                     self._to_device(self._query_start(counts)), path, path_len,
+                     stream=self.stream)
+        kept = path_len.tolist()
+        lens = [self.bm.seq_len(s) - int(n) + int(k) for s, n, k in zip(seq_ids, counts, kept)]
+        for s, n in zip(seq_ids, lens):
+            self.bm.truncate(s, n)
+        return lens

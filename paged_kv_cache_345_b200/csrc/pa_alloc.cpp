@@ -330,6 +330,22 @@ int pa_bm_append_slots(pa_bm* bm, const int32_t* seq_ids, const int32_t* counts,
   return PA_OK;
 }
 
+int pa_bm_truncate(pa_bm* bm, int32_t seq_id, int32_t new_len) {
+  if (!bm) return pa_fail(PA_ERR_INVALID, "pa_bm_truncate: null manager");
+  Seq* s = bm->get(seq_id);
+  if (!s) return pa_fail(PA_ERR_INVALID, "pa_bm_truncate: unknown sequence %d", seq_id);
+  if (new_len < 0 || new_len > s->length)
+    return pa_fail(PA_ERR_INVALID, "pa_bm_truncate: new length %d outside [0, %lld]", new_len,
+                   static_cast<long long>(s->length));
+  const size_t keep = static_cast<size_t>(ceil_div(new_len, bm->block_size));
+  while (s->blocks.size() > keep) {  // last first: the next append takes them back in order
+    pa_decref(bm->pool, s->blocks.back());
+    s->blocks.pop_back();
+  }
+  s->length = new_len;
+  return PA_OK;
+}
+
 int pa_bm_block_tables(const pa_bm* bm, const int32_t* seq_ids, int n, int32_t* tables,
                        int max_blocks_per_seq, int32_t* context_lens) {
   if (!bm || n < 0 || (n > 0 && (!seq_ids || !tables)) || max_blocks_per_seq <= 0)

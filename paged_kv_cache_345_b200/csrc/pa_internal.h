@@ -110,6 +110,63 @@ cudaError_t launch_prefix_attention(int num_seqs, int num_heads, int num_kv_head
                                     const int32_t* block_tables, float* ws_m, float* ws_l,
                                     float* ws_acc, int ws_slots, cudaStream_t stream);
 
+// ---- decode steps with drafted tokens (pa_draft.cu, pa_tree.cu)
+
+// Sizes of one pa_qk_norm_rope_append call after validation.
+struct QkRowsShape {
+  int64_t q_out_stride, q_stride, k_stride, v_stride;  // elements between tokens
+  int64_t num_slots;
+  int num_tokens, num_heads, num_kv_heads, head_dim, max_position, rotary_dim;
+  bool interleaved;
+  float eps;
+  pa_dtype dtype;  // of the cache
+};
+cudaError_t launch_qk_norm_rope_append(const QkRowsShape& sh, void* q_out, const void* q,
+                                       const void* k, const void* v, const int32_t* positions,
+                                       const int64_t* slot_mapping, const float* cos_sin,
+                                       const void* q_weight, const void* k_weight, void* k_cache,
+                                       void* v_cache, const float* k_scale, const float* v_scale,
+                                       cudaStream_t stream);
+
+// Sizes of one pa_verify_draft call after validation.
+struct VerifyShape {
+  int64_t target_stride, draft_stride;  // floats between rows
+  int num_seqs, total_rows, vocab, max_query_len;
+};
+cudaError_t launch_verify_draft(const VerifyShape& sh, int32_t* out_tokens, int32_t* out_path,
+                                int32_t* out_len, const float* target, const float* draft,
+                                const int32_t* tokens, const int32_t* parents,
+                                const int32_t* query_start, const float* u_accept,
+                                const float* u_sample, cudaStream_t stream);
+
+cudaError_t launch_kv_accept(void* k_cache, void* v_cache, const int32_t* block_tables,
+                             const int32_t* context_lens, const int32_t* query_start,
+                             const int32_t* path, const int32_t* path_len, int num_seqs,
+                             int max_path, int num_blocks, int log2_block_size,
+                             int max_blocks_per_seq, int row_bytes, cudaStream_t stream);
+
+// Sizes of one pa_decode_tree call after validation.
+struct TreeShape {
+  int num_seqs, total_q, num_heads, num_kv_heads, head_dim, block_size, num_blocks;
+  int max_blocks_per_seq, max_query_len;
+  float scale;
+};
+// Byte offsets of the regions of a pa_decode_tree workspace.
+struct TreeWorkspace {
+  size_t m_off, l_off, acc_off, total;
+  int slots;      // partial results (two a CTA)
+  int slot_rows;  // rows of one
+};
+// Query tiles of 128 rows a CTA of the tree kernel takes at once (1 or 2), and
+// its CTAs.
+int tree_query_tiles(int num_heads, int num_kv_heads, int max_query_len);
+int tree_ctas(int query_tiles);
+TreeWorkspace tree_workspace(int num_heads, int num_kv_heads, int head_dim, int max_query_len);
+cudaError_t launch_decode_tree(const TreeShape& sh, void* out, const void* q, const void* k_cache,
+                               const void* v_cache, const int32_t* block_tables,
+                               const int32_t* context_lens, const int32_t* query_start,
+                               const int32_t* parents, void* workspace, cudaStream_t stream);
+
 // Device error word of the current device (address in device memory).
 cudaError_t device_error_word(unsigned int** ptr);
 

@@ -11,6 +11,7 @@
 #include "pa_decode_mma.cuh"
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_launch.cuh"
 
 namespace pa {
 
@@ -77,25 +78,6 @@ cudaError_t device_error_word(unsigned int** ptr) {
   cudaError_t e = cache.get(&g_error_word, &addr);
   if (e == cudaSuccess) *ptr = static_cast<unsigned int*>(addr);
   return e;
-}
-
-// Launch with programmatic stream serialization: the kernel may start while
-// the previous kernel in the stream drains; it calls pdl_wait() before reading
-// anything that kernel could have written.
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
-                       cudaStream_t stream, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // ------------------------------------------------------------------ append
@@ -331,19 +313,6 @@ cudaError_t encode_cache_map(CUtensorMap* map, const void* base, const DecodeSha
                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-// Sets a kernel's dynamic shared-memory limit once per device.
-template <typename Kernel>
-cudaError_t ensure_smem(Kernel kernel, int bytes, std::atomic<unsigned long long>& configured) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev % 64);
-  if (configured.load(std::memory_order_acquire) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) configured.fetch_or(bit, std::memory_order_acq_rel);
-  return e;
 }
 
 template <typename T, int D>

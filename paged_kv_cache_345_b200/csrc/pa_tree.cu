@@ -1,0 +1,800 @@
+// Attention of drafted tokens over the paged cache: every sequence's last n
+// tokens form a tree (or a chain), and each attends the tokens before the step,
+// itself and its ancestors. bf16, head_dim 64 or 128, on the 5th-generation
+// tensor cores. ("Paged Attention", klaylearn.com glossary, definition: the
+// kernel reads K and V through the block table; the attention arithmetic is
+// unchanged.)
+//
+// What bounds it: n rows x G query heads of a KV head share each K/V row, 4 d n G
+// flops per 4 d bytes, so up to about 240 rows a KV head it is the cache's
+// bytes. The rows are the M side of the MMA (a tile of 128, row = token * G +
+// head of the group), the keys of a 64-key tile the N side.
+//
+// Work is counted in units, one 64-key tile for one KV head and one item of
+// query rows (QT tiles of 128), ordered by sequence, KV head, item, key. A fixed
+// number of CTAs take equal, contiguous runs of units (each finds its own from
+// the context lengths, so that a captured call follows them), whatever the
+// lengths are: a run may end inside one (sequence, head, item) and start inside
+// another. A run that holds all key tiles of its item writes the output;
+// otherwise (m, l, O) go to the workspace (two slots a CTA: the item it starts
+// inside, and the item it ends inside) with a header, and the merge kernel
+// combines the parts of an item in key order. So the result depends on the
+// lengths of the batch (which set the cuts), not on placement or block size.
+//
+// One CTA:
+//  * warp 0 / warp 1 (producers): K (and Q) / V tiles by TMA, boxes of {64
+//    columns, min(block_size, 64) tokens} with the 128-byte swizzle, into one
+//    ring of 64-key granules (K, V, K, V, ...), running ahead across items.
+//  * warp 2: S_x = Q_x K^T (M 128, N 64), two tiles ahead; warp 3: O_x += P_x V.
+//  * 4 QT softmax warps, thread = row: as in the prefill kernel (base-2
+//    exponentials against a reference that moves when exceeded by 2^8, P in
+//    tensor memory over its S). P is rounded to bf16 (the type of V), and the row
+//    sum adds the rounded weights, so that they sum to 1 exactly.
+// QT = 1 fits two CTAs on an SM (two streams of loads and two softmaxes to hide
+// each other's latency); QT = 2 reads each K/V tile once for 256 rows.
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+#include "pa_launch.cuh"
+#include "pa_prefill_order.h"
+#include "pa_tc.cuh"
+
+namespace pa {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+constexpr int kTreeKeys = 64;    // keys per tile
+constexpr int kTreeRows = 128;   // rows per query tile
+constexpr int kTreeMinUnits = 2; // least units a CTA takes
+
+// What one partial result belongs to: item `item` (KV head * items + item of
+// rows) of sequence s, split over CTAs first .. last; first < 0: none.
+struct TreeHeader {
+  int s, h, row_item, first, last, pad[3];
+};
+
+struct TreeParams {
+  __nv_bfloat16* out;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;
+  const int32_t* parents;
+  unsigned* err;
+  TreeHeader* hdr;  // [CTAs][2]
+  float* ws_m;      // [CTAs][2][slot_rows]
+  float* ws_l;
+  float* ws_acc;    // [CTAs][2][D / 4][slot_rows][4]
+  int num_heads, num_kv_heads, lg_group, block_size, log2_block_size, num_blocks;
+  int max_blocks_per_seq, num_seqs, total_q, max_query_len, slot_rows;
+  int q_box_tokens;  // tokens of a query tile that are loaded
+  float q_scale;     // scale * log2(e)
+};
+
+template <int D, int QT>
+struct TreeConfig {
+  static constexpr int kQBytes = kTreeRows * D * 2;
+  static constexpr int kQHalf = kTreeRows * 128;       // a 64-column half of a Q tile
+  static constexpr int kGran = kTreeKeys * D * 2;      // one K or V tile
+  static constexpr int kGranHalf = kTreeKeys * 128;
+  static constexpr int kHalves = D / 64;
+  static constexpr int kNG = QT == 1 ? (D == 128 ? 5 : 10) : (D == 128 ? 10 : 12);
+  static constexpr int kRing = QT * kQBytes;
+  static constexpr int kBars = kRing + kNG * kGran;
+  static constexpr int kNumBars = 2 * kNG + 2 + 6 * QT;
+  static constexpr int kScratch = kBars + kNumBars * 8;  // tensor-memory address, then the work search
+  static constexpr int kSmemBytes = kScratch + 256;
+  static constexpr int kThreads = 128 + 128 * QT;
+  static constexpr uint32_t kTmemCols = QT == 1 ? 256 : 512;
+  static_assert(2 * 64 * QT + D * QT <= static_cast<int>(kTmemCols), "S and O fit");
+  static_assert(kSmemBytes <= (QT == 1 ? 115712 : 232448), "CTAs per SM");
+};
+
+__device__ __forceinline__ void tree_tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
+                                            int c2, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+
+// A sequence's rows and key tiles; nt = 0: no work (or bad arguments).
+struct TreeSeq {
+  int q0, n, L, nt, items;
+  bool bad;
+};
+
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, int item_tokens) {
+  TreeSeq t{};
+  t.q0 = __ldg(p.query_start + s);
+  const int q1 = __ldg(p.query_start + s + 1);
+  t.L = __ldg(p.context_lens + s);
+  if (!prefill_order::chunk_ok(t.q0, q1, t.L, p.total_q, p.max_query_len,
+                               static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size)) {
+    t.bad = true;
+    return t;
+  }
+  t.n = q1 - t.q0;
+  if (t.n == 0) return t;
+  t.nt = (t.L + kTreeKeys - 1) / kTreeKeys;
+  t.items = (t.n + item_tokens - 1) / item_tokens;
+  return t;
+}
+
+__device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& t) {
+  return static_cast<int64_t>(t.nt) * t.items * p.num_kv_heads;
+}
+
+// One run of key tiles of one item.
+struct TreeRun {
+  int s, q0, n, L, nt, h, row_item, t0, t1;
+  int64_t item_unit;  // the item's first unit
+};
+
+// Calls f(run) for each run of the units [u0, u1), from sequence s on, whose
+// units start at `base`; stops when f returns false.
+template <typename F>
+__device__ __forceinline__ void tree_runs(const TreeParams& p, int64_t u0, int64_t u1, int s,
+                                          int64_t base, int item_tokens, F&& f) {
+  int64_t u = u0;
+  while (u < u1 && s < p.num_seqs) {
+    const TreeSeq t = tree_seq(p, s, item_tokens);
+    const int64_t units = tree_units(p, t);
+    while (u < u1 && u - base < units) {
+      const int64_t item = (u - base) / t.nt;
+      TreeRun r;
+      r.s = s;
+      r.q0 = t.q0;
+      r.n = t.n;
+      r.L = t.L;
+      r.nt = t.nt;
+      r.h = static_cast<int>(item / t.items);
+      r.row_item = static_cast<int>(item - static_cast<int64_t>(r.h) * t.items);
+      r.item_unit = base + item * t.nt;
+      r.t0 = static_cast<int>(u - r.item_unit);
+      r.t1 = static_cast<int>(min(static_cast<int64_t>(t.nt), r.t0 + (u1 - u)));
+      if (!f(r)) return;
+      u += r.t1 - r.t0;
+    }
+    base += units;
+    ++s;
+  }
+}
+
+// A place in the ring of granules: its index and the parity of its use.
+struct RingPos {
+  int st;
+  uint32_t ph;
+  template <int NG>
+  __device__ __forceinline__ void step2() {  // two granules on
+    st += 2;
+    if (st >= NG) {
+      st -= NG;
+      ph ^= 1;
+    }
+  }
+};
+
+template <int D, int QT>
+__global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
+    pa_tree_kernel(const __grid_constant__ CUtensorMap q_map,
+                   const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map, const TreeParams p) {
+  using Cfg = TreeConfig<D, QT>;
+  constexpr int NG = Cfg::kNG, KEYN = kTreeKeys, HALVES = Cfg::kHalves;
+  extern __shared__ __align__(1024) uint8_t sm[];
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::kBars);
+  auto bar = [&](int i) { return smem_u32(bars + i); };
+  // barriers: a granule full, empty; Q full, empty; per query tile and parity of
+  // the tile count: S full, P full, P V done
+  constexpr int kFull = 0, kEmpty = NG, kQFull = 2 * NG, kQEmpty = 2 * NG + 1, kS = 2 * NG + 2;
+  constexpr int kP = kS + 2 * QT, kO = kP + 2 * QT;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::kScratch);
+  int64_t* s_sum = reinterpret_cast<int64_t*>(sm + Cfg::kScratch + 16);  // [12] per warp, then total
+  int64_t* s_base = s_sum + 13;
+  int* s_seq = reinterpret_cast<int*>(s_sum + 14);
+  auto q_s = [&](int x) { return smem_u32(sm + x * Cfg::kQBytes); };
+  auto gran = [&](int st) { return smem_u32(sm + Cfg::kRing) + st * Cfg::kGran; };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = 1 << p.lg_group, TOK = kTreeRows >> p.lg_group;
+  const int item_tokens = QT * TOK;
+  const int bs = p.block_size, lg = p.log2_block_size;
+  auto wait_all = [&](uint32_t b, uint32_t parity) {
+    return __all_sync(kFullMask, mbar_wait(b, parity, p.err));
+  };
+
+  if (smem_u32(sm) & 1023) {  // the swizzled operand layout needs this
+    if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NG; ++i) {
+      mbar_init(bar(kFull + i), 1);
+      mbar_init(bar(kEmpty + i), 1);
+    }
+    mbar_init(bar(kQFull), 1);
+    mbar_init(bar(kQEmpty), 1);
+    for (int i = 0; i < 2 * QT; ++i) {
+      mbar_init(bar(kS + i), 1);
+      mbar_init(bar(kP + i), 128);
+      mbar_init(bar(kO + i), 1);
+    }
+    fence_barrier_init();
+    prefetch_tensormap(&q_map);
+    prefetch_tensormap(&k_map);
+    prefetch_tensormap(&v_map);
+  }
+  if (warp == 2) tc::tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
+  pdl_wait();  // inputs may come from the previous kernel in the stream
+  pdl_launch_dependents();
+
+  // The units of the batch, then this CTA's run and the sequence it starts in.
+  // Scans of kThreads sequences at a time, each thread one.
+  constexpr int NT = Cfg::kThreads, NW = NT / 32;
+  int64_t total = 0;
+  for (int s0 = 0; s0 < p.num_seqs; s0 += NT) {
+    const int s = s0 + threadIdx.x;
+    if (s < p.num_seqs) {
+      const TreeSeq t = tree_seq(p, s, item_tokens);
+      if (t.bad && blockIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT);
+      total += tree_units(p, t);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
+  if (lane == 0) s_sum[warp] = total;
+  if (threadIdx.x == 0) *s_seq = p.num_seqs;
+  __syncthreads();
+  total = 0;
+  for (int w = 0; w < NW; ++w) total += s_sum[w];
+  int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < kTreeMinUnits) share = kTreeMinUnits;
+  const int64_t u0 = blockIdx.x * share, u1 = min(u0 + share, total);
+  if (u0 < u1) {
+    int64_t before = 0;
+    for (int s0 = 0; s0 < p.num_seqs && before <= u0; s0 += NT) {
+      const int s = s0 + threadIdx.x;
+      const int64_t mine = s < p.num_seqs ? tree_units(p, tree_seq(p, s, item_tokens)) : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(kFullMask, incl, o);
+        if (lane >= o) incl += v;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      int64_t chunk = 0;
+      for (int w = 0; w < NW; ++w) {
+        if (w < warp) incl += s_sum[w];
+        chunk += s_sum[w];
+      }
+      if (before + incl - mine <= u0 && u0 < before + incl) {
+        *s_seq = s;
+        *s_base = before + incl - mine;
+      }
+      before += chunk;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const int seq0 = *s_seq;
+  const int64_t base0 = *s_base;
+  auto t_s = [&](int x, int b) { return tmem + (2 * x + b) * KEYN; };
+  auto t_o = [&](int x) { return tmem + 2 * QT * KEYN + x * D; };
+  auto runs = [&](auto&& f) {
+    if (u0 < u1) tree_runs(p, u0, u1, seq0, base0, item_tokens, f);
+  };
+
+  if (warp < 2) {
+    // ------------------------------------------------- producers: K and Q, V
+    const CUtensorMap* map = warp == 0 ? &k_map : &v_map;
+    const int rows = bs < KEYN ? bs : KEYN, lgr = bs < KEYN ? lg : 6;  // tokens per box
+    RingPos pos{warp, 0};
+    uint32_t qph = 0;
+    runs([&](const TreeRun& r) {
+      if (warp == 0) {
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
+          if (ok) {
+            const int box = p.q_box_tokens * G * 128;
+            mbar_arrive_expect_tx(bar(kQFull), QT * HALVES * box);
+            for (int x = 0; x < QT; ++x)
+              for (int c = 0; c < HALVES; ++c)
+                tree_tma_3d(q_s(x) + c * Cfg::kQHalf, &q_map, c * 64, r.h * G,
+                            r.q0 + r.row_item * item_tokens + x * TOK, bar(kQFull));
+          }
+        }
+        if (!__shfl_sync(kFullMask, ok, 0)) return false;
+        qph ^= 1;
+      }
+      const int32_t* trow = p.block_tables + static_cast<int64_t>(r.s) * p.max_blocks_per_seq;
+      for (int t = r.t0; t < r.t1; ++t) {
+        const int key0 = t * KEYN;
+        const int nkeys = min(KEYN, r.L - key0);
+        const int nbox = (nkeys + rows - 1) >> lgr;  // <= 8
+        const int b = lane % nbox;
+        int blk = 0;
+        if (lane < nbox * HALVES) blk = __ldg(trow + ((key0 + b * rows) >> lg));
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait(bar(kEmpty + pos.st), pos.ph ^ 1, p.err);
+          if (ok) mbar_arrive_expect_tx(bar(kFull + pos.st), static_cast<uint32_t>(nbox * rows * 128 * HALVES));
+        }
+        if (!__shfl_sync(kFullMask, ok, 0)) return false;
+        if (lane < nbox * HALVES) {
+          // an id outside the pool is flagged; TMA reads an out-of-range box as zeros
+          if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks))
+            atomicOr(p.err, PA_DEVERR_BLOCK_ID);
+          const int half = lane >= nbox;
+          tma_load_4d(gran(pos.st) + half * Cfg::kGranHalf + b * rows * 128, map, half * 64,
+                      (key0 + b * rows) & (bs - 1), r.h, blk, bar(kFull + pos.st));
+        }
+        pos.step2<NG>();
+      }
+      return true;
+    });
+  } else if (warp == 2) {
+    // -------------------------------------------------------- S = Q K^T MMAs
+    constexpr uint32_t kIdS = tc::idesc_bf16_f32(kTreeRows, KEYN, 0);
+    RingPos pos{0, 0};
+    uint32_t qph = 0;
+    int it = 0;  // tiles so far, over all runs
+    runs([&](const TreeRun& r) {
+      if (!wait_all(bar(kQFull), qph)) return false;
+      qph ^= 1;
+      for (int t = r.t0; t < r.t1; ++t, ++it) {
+        // this buffer of S held P of tile it - 2 until its P V was done
+        if (it >= 2)
+          for (int x = 0; x < QT; ++x)
+            if (!wait_all(bar(kO + 2 * x + (it & 1)), ((it - 2) >> 1) & 1)) return false;
+        if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint32_t kb = gran(pos.st);
+#pragma unroll
+          for (int x = 0; x < QT; ++x) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks)
+              tc::mma_bf16(t_s(x, it & 1),
+                           tc::smem_desc_sw128(q_s(x) + (ks >> 2) * Cfg::kQHalf + (ks & 3) * 32, 16, 1024),
+                           tc::smem_desc_sw128(kb + (ks >> 2) * Cfg::kGranHalf + (ks & 3) * 32, 16, 1024),
+                           kIdS, ks > 0);
+            tc::commit(bar(kS + 2 * x + (it & 1)));
+          }
+          tc::commit(bar(kEmpty + pos.st));
+          if (t == r.t1 - 1) tc::commit(bar(kQEmpty));
+        }
+        __syncwarp();
+        pos.step2<NG>();
+      }
+      return true;
+    });
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ P V MMAs
+    constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
+    RingPos pos{1, 0};
+    int it = 0;
+    runs([&](const TreeRun& r) {
+      for (int t = r.t0; t < r.t1; ++t, ++it) {
+        if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
+        const uint32_t vb = gran(pos.st);
+        for (int x = 0; x < QT; ++x) {
+          if (!wait_all(bar(kP + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
+          tc::fence_after_sync();
+          if (lane == 0) {
+#pragma unroll
+            for (int ks = 0; ks < KEYN / 16; ++ks)
+              tc::mma_bf16_tmem_a(t_o(x), t_s(x, it & 1) + ks * 8,
+                                  tc::smem_desc_sw128(vb + ks * 2048, Cfg::kGranHalf, 1024), kIdPV,
+                                  t > r.t0 || ks > 0);
+            tc::commit(bar(kO + 2 * x + (it & 1)));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) tc::commit(bar(kEmpty + pos.st));
+        __syncwarp();
+        pos.step2<NG>();
+      }
+      return true;
+    });
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int x = (warp - 4) >> 2;  // query tile of this warpgroup
+    const int wq = warp & 3;        // tensor-memory lanes 32 wq .. 32 wq + 31
+    const int r_ = wq * 32 + lane;  // row
+    const int tok = r_ >> p.lg_group, g = r_ & (G - 1);
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const float qs = p.q_scale;
+    RingPos vpos{1, 0};
+    int it = 0;
+    TreeHeader none{};
+    none.first = -1;
+    const bool teller = warp == 4 && lane == 0;
+    TreeHeader* hdr = p.hdr + 2 * blockIdx.x;
+    if (teller) hdr[0] = hdr[1] = none;
+    runs([&](const TreeRun& r) {
+      const int my_tok = r.row_item * item_tokens + x * TOK + tok;  // token of this sequence's n
+      const bool real = my_tok < r.n;
+      // (warps without a row compute nothing, but take part in every barrier)
+      const bool warp_real = (r.row_item * item_tokens + x * TOK + ((wq * 32) >> p.lg_group)) < r.n;
+      const int before = r.L - r.n;  // tokens every row sees
+      float m_use = -INFINITY, l_run = 0.0f;
+      for (int t = r.t0; t < r.t1; ++t, ++it) {
+        if (!wait_all(bar(kS + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
+        tc::fence_after_sync();
+        const int key0 = t * KEYN;
+        float alpha = 1.0f;
+        uint32_t pw[KEYN / 2];
+        if (warp_real) {
+          uint32_t sv[2][32];
+          tc::ld32(t_s(x, it & 1) + lane_off, sv[0]);
+          tc::ld32(t_s(x, it & 1) + lane_off + 32, sv[1]);
+          tc::wait_ld();
+          if (key0 + KEYN > before) {
+            // bit i: key key0 + i is seen. Keys before the step, then the row's
+            // own and its ancestors' (a parent comes before its child).
+            const int rel = key0 - before;  // row of the step that key 0 of the tile is
+            uint64_t seen = rel >= 0 ? 0ull : rel <= -64 ? ~0ull : (1ull << -rel) - 1;
+            if (real) {
+              if (p.parents == nullptr) {
+                const int top = my_tok - rel;  // a chain: every earlier row
+                if (top >= 63) seen = ~0ull;
+                else if (top >= 0) seen |= (2ull << top) - 1;
+              } else {
+                int a = my_tok;
+                while (a >= 0 && a >= rel) {
+                  if (a - rel < 64) seen |= 1ull << (a - rel);
+                  const int up = __ldg(p.parents + r.q0 + a);
+                  if (up >= a || up < -1) {
+                    atomicOr(p.err, PA_DEVERR_DRAFT);
+                    break;
+                  }
+                  a = up;
+                }
+              }
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t bits = static_cast<uint32_t>(seen >> (32 * c));
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!((bits >> i) & 1)) sv[c][i] = 0xff800000u;  // -inf
+            }
+          }
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sv[c][i]));
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs;
+          const bool move = mx > m_use + 8.0f;
+          const float m_new = move ? mx : m_use;
+          alpha = move ? exp2_fast(m_use - m_new) : 1.0f;
+          // a row that has seen no key yet keeps m = -inf and weights of 0
+          const float m_sub = m_new == -INFINITY ? 0.0f : m_new;
+          float rs0 = 0.0f, rs1 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < KEYN / 2; ++e) {
+            const int i0 = 2 * e;
+            const float a = exp2_fast(fmaf(__uint_as_float(sv[i0 >> 5][i0 & 31]), qs, -m_sub));
+            const float b = exp2_fast(fmaf(__uint_as_float(sv[(i0 + 1) >> 5][(i0 + 1) & 31]), qs, -m_sub));
+            pw[e] = pack_bf16x2(a, b);
+            rs0 += __uint_as_float(pw[e] << 16);
+            rs1 += __uint_as_float(pw[e] & 0xffff0000u);
+          }
+          l_run = l_run * alpha + (rs0 + rs1);
+          m_use = m_new;
+        }
+        const bool rescale = t > r.t0 && __any_sync(kFullMask, alpha != 1.0f);
+        if (rescale) {
+          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return false;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tc::ld32(t_o(x) + lane_off + c * 32, ov);
+            tc::wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
+            tc::st32(t_o(x) + lane_off + c * 32, ov);
+          }
+        }
+        if (warp_real) {
+          tc::st32(t_s(x, it & 1) + lane_off, pw);
+          tc::wait_st();
+        }
+        if (x == 0 && key0 + KEYN > r.L) {
+          // keys past the context: stale or unwritten V rows become zeros (their
+          // P is 0, but 0 * NaN would not be)
+          if (!wait_all(bar(kFull + vpos.st), vpos.ph)) return false;
+          const int nkeys = r.L - key0;
+          const uint32_t vb = gran(vpos.st);
+          constexpr int kVecs = 8 * HALVES;
+          for (int i = r_; i < (KEYN - nkeys) * kVecs; i += 128) {
+            const int row = nkeys + i / kVecs, c = i % kVecs;
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             vb + (c >> 3) * Cfg::kGranHalf + row * 128 + ((c & 7) << 4)),
+                         "r"(0u)
+                         : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        vpos.step2<NG>();
+        tc::fence_before_sync();
+        mbar_arrive(bar(kP + 2 * x + (it & 1)));
+        if (t > r.t0 && !rescale) {
+          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return false;
+        }
+      }
+      // the run's end: O of all its tiles
+      if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return false;
+      tc::fence_after_sync();
+      if (!warp_real) return true;
+      if (r.t0 == 0 && r.t1 == r.nt) {
+        const float inv = 1.0f / l_run;
+        __nv_bfloat16* dst =
+            p.out + ((static_cast<int64_t>(r.q0) + my_tok) * p.num_heads + (r.h << p.lg_group) + g) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tc::ld32(t_o(x) + lane_off + c * 32, ov);
+          tc::wait_ld();
+          if (real) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint4 w;
+              w.x = pack_bf16x2(__uint_as_float(ov[8 * v]) * inv, __uint_as_float(ov[8 * v + 1]) * inv);
+              w.y = pack_bf16x2(__uint_as_float(ov[8 * v + 2]) * inv, __uint_as_float(ov[8 * v + 3]) * inv);
+              w.z = pack_bf16x2(__uint_as_float(ov[8 * v + 4]) * inv, __uint_as_float(ov[8 * v + 5]) * inv);
+              w.w = pack_bf16x2(__uint_as_float(ov[8 * v + 6]) * inv, __uint_as_float(ov[8 * v + 7]) * inv);
+              *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = w;
+            }
+          }
+        }
+      } else {
+        // a part of an item: [D / 4][rows][4] so that a warp's stores are whole lines
+        const int side = r.t0 > 0 ? 0 : 1;
+        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + side;
+        const int row = x * kTreeRows + r_;
+        if (real) {
+          p.ws_m[slot * p.slot_rows + row] = m_use;
+          p.ws_l[slot * p.slot_rows + row] = l_run;
+        }
+        float* dst = p.ws_acc + (slot * D * p.slot_rows) + row * 4;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t ov[32];
+          tc::ld32(t_o(x) + lane_off + c * 32, ov);
+          tc::wait_ld();
+          if (real) {
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(c * 8 + v) * p.slot_rows * 4) =
+                  make_uint4(ov[4 * v], ov[4 * v + 1], ov[4 * v + 2], ov[4 * v + 3]);
+          }
+        }
+        if (teller) {
+          TreeHeader hd{};
+          hd.s = r.s;
+          hd.h = r.h;
+          hd.row_item = r.row_item;
+          hd.first = static_cast<int>(r.item_unit / share);
+          hd.last = static_cast<int>((r.item_unit + r.nt - 1) / share);
+          hdr[side] = hd;
+        }
+      }
+      // (the next run's first P V overwrites O once P of its first tile is
+      // published, which these threads do after the loads above)
+      return true;
+    });
+  }
+
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 2) tc::tmem_dealloc(tmem, Cfg::kTmemCols);
+}
+
+// Merge of the items that were split: the CTAs that held a part of one share
+// its columns (in fours), each thread one row of four columns over all parts in
+// key order:
+//   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j.
+template <int D>
+__global__ void __launch_bounds__(512) tree_merge_kernel(const TreeParams p, int query_tiles) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int slot = blockIdx.x, cta = slot >> 1;
+  const TreeHeader hd = p.hdr[slot];
+  if (hd.first < 0) return;
+  const int rank = cta - hd.first, parts = hd.last - hd.first + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = 1 << p.lg_group;
+  const int q0 = __ldg(p.query_start + hd.s), n = __ldg(p.query_start + hd.s + 1) - q0;
+  const int tok0 = hd.row_item * query_tiles * (kTreeRows >> p.lg_group);
+  const int rows = min(query_tiles * kTreeRows, (n - tok0) * G);
+  const int groups = (rows + 31) / 32;               // of 32 rows
+  const int cols = (D / 4 - rank + parts - 1) / parts;  // this CTA's columns: rank, rank + parts, ...
+  for (int w = warp; w < groups * cols; w += 16) {
+    const int row = (w % groups) * 32 + lane, col = rank + (w / groups) * parts;
+    if (row >= rows) continue;
+    float M = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int B = 8;
+    for (int j0 = 0; j0 < parts; j0 += B) {
+      float mq[B], lq[B];
+      float4 vq[B];
+#pragma unroll
+      for (int j = 0; j < B; ++j) {  // (a place past the last part loads that part again)
+        const int k = min(j0 + j, parts - 1);
+        // the first part lies in its CTA's second slot, the others in the first
+        const int64_t sl = 2 * static_cast<int64_t>(hd.first + k) + (k == 0 ? 1 : 0);
+        mq[j] = ld_cg_f32(p.ws_m + sl * p.slot_rows + row);
+        lq[j] = ld_cg_f32(p.ws_l + sl * p.slot_rows + row);
+        vq[j] = ld_cg_f32x4(p.ws_acc + (sl * (D / 4) + col) * p.slot_rows * 4 + row * 4);
+      }
+      float bm = M;
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        if (j0 + j >= parts) mq[j] = -INFINITY;
+        bm = fmaxf(bm, mq[j]);
+      }
+      if (bm == -INFINITY) continue;  // this row saw no key in these parts
+      const float sc = exp2f(M - bm);
+      l *= sc;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] *= sc;
+#pragma unroll
+      for (int j = 0; j < B; ++j) {
+        // (a part without a key for this row may hold 0 * stale sums: left out)
+        if (mq[j] == -INFINITY) continue;
+        const float wt = exp2f(mq[j] - bm);
+        l = fmaf(wt, lq[j], l);
+        acc[0] = fmaf(wt, vq[j].x, acc[0]);
+        acc[1] = fmaf(wt, vq[j].y, acc[1]);
+        acc[2] = fmaf(wt, vq[j].z, acc[2]);
+        acc[3] = fmaf(wt, vq[j].w, acc[3]);
+      }
+      M = bm;
+    }
+    const float inv = 1.0f / l;
+    const int tok = tok0 + (row >> p.lg_group);
+    __nv_bfloat16* dst = p.out + ((static_cast<int64_t>(q0) + tok) * p.num_heads +
+                                  (hd.h << p.lg_group) + (row & (G - 1))) * D + col * 4;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  }
+}
+
+cudaError_t encode_tree_q(CUtensorMap* map, const void* q, int total_q, int num_heads, int head_dim,
+                          int group, int box_tokens) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_heads),
+                              static_cast<cuuint64_t>(total_q)};
+  const cuuint64_t strides[2] = {row, static_cast<cuuint64_t>(num_heads) * row};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Cache [num_blocks][block_size][Hkv][D] viewed (column, token, head, block).
+cudaError_t encode_tree_kv(CUtensorMap* map, const void* base, const TreeShape& sh, int rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t row = static_cast<cuuint64_t>(sh.head_dim) * 2;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(sh.head_dim), static_cast<cuuint64_t>(sh.block_size),
+                              static_cast<cuuint64_t>(sh.num_kv_heads),
+                              static_cast<cuuint64_t>(sh.num_blocks)};
+  const cuuint64_t strides[3] = {row * sh.num_kv_heads, row,
+                                 row * sh.num_kv_heads * static_cast<cuuint64_t>(sh.block_size)};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides,
+                   box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D, int QT>
+cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* q, const void* k_cache,
+                          const void* v_cache, cudaStream_t stream) {
+  using Cfg = TreeConfig<D, QT>;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = ensure_smem(pa_tree_kernel<D, QT>, Cfg::kSmemBytes, configured);
+  if (e != cudaSuccess) return e;
+  CUtensorMap qmap, kmap, vmap;
+  const int rows = sh.block_size < kTreeKeys ? sh.block_size : kTreeKeys;
+  if ((e = encode_tree_q(&qmap, q, sh.total_q, sh.num_heads, D, 1 << p.lg_group, p.q_box_tokens)) != cudaSuccess) return e;
+  if ((e = encode_tree_kv(&kmap, k_cache, sh, rows)) != cudaSuccess) return e;
+  if ((e = encode_tree_kv(&vmap, v_cache, sh, rows)) != cudaSuccess) return e;
+  const unsigned ctas = static_cast<unsigned>(tree_ctas(QT));
+  e = launch_pdl(pa_tree_kernel<D, QT>, dim3(ctas), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
+                 qmap, kmap, vmap, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(tree_merge_kernel<D>, dim3(2 * ctas), dim3(512), 0, stream, p, QT);
+}
+
+}  // namespace
+
+int tree_query_tiles(int num_heads, int num_kv_heads, int max_query_len) {
+  const int64_t rows = static_cast<int64_t>(max_query_len) * (num_heads / num_kv_heads);
+  return rows > kTreeRows ? 2 : 1;
+}
+
+int tree_ctas(int query_tiles) { return query_tiles == 1 ? 2 * 148 : 148; }
+
+TreeWorkspace tree_workspace(int num_heads, int num_kv_heads, int head_dim, int max_query_len) {
+  TreeWorkspace w{};
+  const int qt = tree_query_tiles(num_heads, num_kv_heads, max_query_len);
+  const int64_t rows = static_cast<int64_t>(max_query_len) * (num_heads / num_kv_heads);
+  w.slots = 2 * tree_ctas(qt);
+  // (grows with max_query_len: a workspace for more rows serves fewer)
+  w.slot_rows = qt == 2 ? 2 * kTreeRows : static_cast<int>((rows + 31) / 32 * 32);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  const size_t each = static_cast<size_t>(w.slots) * w.slot_rows;
+  w.m_off = up(static_cast<size_t>(2 * tree_ctas(1)) * sizeof(TreeHeader));
+  w.l_off = w.m_off + up(each * sizeof(float));
+  w.acc_off = w.l_off + up(each * sizeof(float));
+  w.total = w.acc_off + each * head_dim * sizeof(float);
+  return w;
+}
+
+cudaError_t launch_decode_tree(const TreeShape& sh, void* out, const void* q, const void* k_cache,
+                               const void* v_cache, const int32_t* block_tables,
+                               const int32_t* context_lens, const int32_t* query_start,
+                               const int32_t* parents, void* workspace, cudaStream_t stream) {
+  const TreeWorkspace w =
+      tree_workspace(sh.num_heads, sh.num_kv_heads, sh.head_dim, sh.max_query_len);
+  TreeParams p{};
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.query_start = query_start;
+  p.parents = parents;
+  cudaError_t e = device_error_word(&p.err);
+  if (e != cudaSuccess) return e;
+  p.hdr = reinterpret_cast<TreeHeader*>(ws);
+  p.ws_m = reinterpret_cast<float*>(ws + w.m_off);
+  p.ws_l = reinterpret_cast<float*>(ws + w.l_off);
+  p.ws_acc = reinterpret_cast<float*>(ws + w.acc_off);
+  p.num_heads = sh.num_heads;
+  p.num_kv_heads = sh.num_kv_heads;
+  const int group = sh.num_heads / sh.num_kv_heads;
+  p.lg_group = group == 1 ? 0 : group == 2 ? 1 : group == 4 ? 2 : 3;
+  p.block_size = sh.block_size;
+  int lg = 0;
+  while ((1 << lg) < sh.block_size) ++lg;
+  p.log2_block_size = lg;
+  p.num_blocks = sh.num_blocks;
+  p.max_blocks_per_seq = sh.max_blocks_per_seq;
+  p.num_seqs = sh.num_seqs;
+  p.total_q = sh.total_q;
+  p.max_query_len = sh.max_query_len;
+  p.slot_rows = w.slot_rows;
+  p.q_box_tokens = sh.max_query_len < kTreeRows / group ? sh.max_query_len : kTreeRows / group;
+  p.q_scale = sh.scale * 1.4426950408889634f;  // log2(e)
+  const int qt = tree_query_tiles(sh.num_heads, sh.num_kv_heads, sh.max_query_len);
+  if (sh.head_dim == 64)
+    return qt == 1 ? launch_tree_t<64, 1>(sh, p, q, k_cache, v_cache, stream)
+                   : launch_tree_t<64, 2>(sh, p, q, k_cache, v_cache, stream);
+  return qt == 1 ? launch_tree_t<128, 1>(sh, p, q, k_cache, v_cache, stream)
+                 : launch_tree_t<128, 2>(sh, p, q, k_cache, v_cache, stream);
+}
+
+}  // namespace pa
