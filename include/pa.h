@@ -590,7 +590,7 @@ int pa_prefill_planned(void* out, const void* q, const void* k_cache, const void
  *                  q, k or v.
  *   k, v           device, [num_tokens][num_kv_heads][head_dim], likewise.
  *   positions      device, int32 [num_tokens]: rotation position. Negative: a
- *                  padding row, nothing of it is read or written. >= max_position
+ *                  padding row, nothing of it is written. >= max_position
  *                  sets PA_DEVERR_POSITION and skips the token.
  *   slot_mapping   device, int64 [num_tokens], as in pa_kv_append (distinct; a
  *                  negative slot writes no K or V, q_out is still written).

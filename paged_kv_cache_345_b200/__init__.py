@@ -211,13 +211,22 @@ def _dev_ptr(t, name, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()   # (an int: ctypes converts it by the argument's declared type)
 
 
 def _stream(stream, device):
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle, without a Stream object for it, where torch offers that
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    index = getattr(device, "index", device)
+    if raw is not None and isinstance(index, int) and torch.cuda.is_initialized():
+        return raw(index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+_NO_GUARD = contextlib.nullcontext()
 
 
 def _on_device(tensors, stream):
@@ -226,15 +235,23 @@ def _on_device(tensors, stream):
     own memory), an explicit stream must belong to that device, and the call
     runs with that device current. CPU tensors (pinned host pools) are skipped."""
     torch = _torch()
-    devs = {t.device for t in tensors if t is not None and t.is_cuda}
-    if len(devs) > 1:
-        raise ValueError("tensors of one call are on several devices: " +
-                         ", ".join(sorted(str(d) for d in devs)))
-    dev = devs.pop() if devs else None
-    if dev is not None and stream is not None and stream.device != dev:
+    dev = None
+    for t in tensors:
+        if t is None or not t.is_cuda:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            devs = {t.device for t in tensors if t is not None and t.is_cuda}
+            raise ValueError("tensors of one call are on several devices: " +
+                             ", ".join(sorted(str(d) for d in devs)))
+    if dev is None:
+        return _NO_GUARD, _stream(stream, None)
+    if stream is not None and stream.device != dev:
         raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
-    guard = torch.cuda.device(dev) if dev is not None else contextlib.nullcontext()
-    return guard, _stream(stream, dev)
+    if torch.cuda.is_initialized() and torch.cuda.current_device() == dev.index:
+        return _NO_GUARD, _stream(stream, dev)      # (already current: nothing to switch)
+    return torch.cuda.device(dev), _stream(stream, dev)
 
 
 # ---------------------------------------------------------------- kernels
@@ -682,7 +699,7 @@ def pa_prefill_plan(query_start, context_lens, num_heads: int, num_kv_heads: int
     return out[:n.value]
 
 
-def _dev_rows(t, name, heads, dtype):
+def _dev_rows(t, name, dtype):
     """(pointer, elements between tokens) of a [N, heads, d] view whose heads are
     dense: a contiguous tensor, or one part of a packed projection."""
     if not t.is_cuda:
@@ -690,9 +707,11 @@ def _dev_rows(t, name, heads, dtype):
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     n, h, d = t.shape
-    if h != heads or (t.numel() and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d))):
-        raise ValueError(f"{name} must be [N, {heads}, head_dim] with dense heads")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if n > 1 else h * d)
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
+        if t.numel():
+            raise ValueError(f"{name} must be [N, heads, head_dim] with dense heads")
+    return t.data_ptr(), (st[0] if n > 1 else h * d)
 
 
 def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
@@ -711,7 +730,8 @@ def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_c
     fp8 = _is_fp8(k_cache)
     dt = torch.bfloat16 if fp8 else k_cache.dtype
     if q.dim() != 3 or k.dim() != 3 or q.shape[2] != d or k.shape[2] != d or \
-            q_out.shape != q.shape or v.shape != k.shape or k.shape[0] != q.shape[0]:
+            q_out.shape != q.shape or v.shape != k.shape or k.shape[0] != q.shape[0] or \
+            k.shape[1] != hkv:
         raise ValueError("q/q_out must be [N, num_heads, head_dim], k/v [N, num_kv_heads, head_dim]")
     n, hq = q.shape[:2]
     if v_cache.shape != k_cache.shape or positions.shape != (n,) or slot_mapping.shape != (n,):
@@ -729,8 +749,8 @@ def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_c
     guard, st = _on_device((q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
                             q_weight, k_weight, k_scale, v_scale), stream)
     with guard:
-        (po, so), (pq, sq) = _dev_rows(q_out, "q_out", hq, dt), _dev_rows(q, "q", hq, dt)
-        (pk, sk), (pv, sv) = _dev_rows(k, "k", hkv, dt), _dev_rows(v, "v", hkv, dt)
+        (po, so), (pq, sq) = _dev_rows(q_out, "q_out", dt), _dev_rows(q, "q", dt)
+        (pk, sk), (pv, sv) = _dev_rows(k, "k", dt), _dev_rows(v, "v", dt)
         _check(_lib.pa_qk_norm_rope_append(
             po, pq, pk, pv, so, sq, sk, sv, _dev_ptr(positions, "positions", torch.int32),
             _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
@@ -793,7 +813,7 @@ def _prob_rows(t, name, rows, vocab):
         raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
     if tuple(t.shape) != (rows, vocab) or (vocab > 1 and t.numel() and t.stride(1) != 1):
         raise ValueError(f"{name} must be [total_q, vocab_size] with dense rows")
-    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if rows > 1 else vocab)
+    return t.data_ptr(), (t.stride(0) if rows > 1 else vocab)
 
 
 def pa_verify_draft(out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens,

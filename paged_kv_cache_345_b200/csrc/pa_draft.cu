@@ -44,7 +44,7 @@ struct RowsParams {
 // Rows of T; a lane holds 16 bytes of a head's row, kLanes lanes a row, so a
 // warp instruction moves kRows rows. A unit of work is U such instructions of
 // one token (its q heads, then k, then v heads); one warp per unit, all its
-// loads first. HBM-bound: every row is read and written once, the cosines and
+// loads first (before the position is known). HBM-bound: every row is read and written once, the cosines and
 // sines of a token once per unit from L1/L2.
 template <typename T, int D>
 struct RowsConfig {
@@ -88,13 +88,6 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
   const int pos = __ldg(p.positions + tok);
   const int64_t slot = __ldg(p.slots + tok);
   const int row0 = static_cast<int>(unit - tok * p.units_per_token) * (U * Cfg::kRows) + lane / LPR;
-  if (pos < 0) return;  // padding
-  if (pos >= p.max_position || slot >= p.num_slots) {
-    if (lane == 0 && row0 == 0)
-      atomicOr(p.err, pos >= p.max_position ? PA_DEVERR_POSITION : PA_DEVERR_SLOT);
-    if (pos >= p.max_position) return;
-  }
-  const bool write_kv = slot >= 0 && slot < p.num_slots;
   const int hq = p.num_heads, hkv = p.num_kv_heads, total = hq + 2 * hkv;
 
   // rows of this unit: kind 0 q, 1 k, 2 v, 3 none
@@ -105,7 +98,6 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
     const int r = row0 + u * Cfg::kRows;
     kind[u] = r < hq ? 0 : r < hq + hkv ? 1 : r < total ? 2 : 3;
     head[u] = kind[u] == 0 ? r : kind[u] == 1 ? r - hq : r - hq - hkv;
-    if (kind[u] != 0 && !write_kv) kind[u] = 3;
     raw[u] = make_uint4(0, 0, 0, 0);
     if (kind[u] != 3) {
       const T* base = static_cast<const T*>(kind[u] == 0 ? p.q : kind[u] == 1 ? p.k : p.v);
@@ -113,6 +105,17 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
       // (not the read-only path: q_out may be q)
       raw[u] = __ldcs(reinterpret_cast<const uint4*>(base + tok * st + head[u] * D + li * EPL));
     }
+  }
+  if (pos < 0) return;  // padding
+  if (pos >= p.max_position || slot >= p.num_slots) {
+    if (lane == 0 && row0 == 0)
+      atomicOr(p.err, pos >= p.max_position ? PA_DEVERR_POSITION : PA_DEVERR_SLOT);
+    if (pos >= p.max_position) return;
+  }
+  if (slot < 0 || slot >= p.num_slots) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (kind[u] != 0) kind[u] = 3;
   }
   // cosines and sines of this lane's elements
   const int half = p.rotary_dim >> 1;
@@ -405,6 +408,7 @@ struct VerifyParams {
 
 constexpr int kVerifyThreads = 512;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyBatch = 4;  // groups of 128 values that a warp loads at once
 
 // The mass left of a target row after the rejections at one node,
 //   sampled drafts: R_0 = p, R_{k+1} = max(R_k / Z_k - q, 0), Z_k = sum R_k (Z_0 = 1).
@@ -435,7 +439,7 @@ __device__ __forceinline__ double mass_of(float p, float q, double a, double b) 
 // piece is then searched by one warp. Bound by reading one row of p and one of
 // q per sequence.
 template <bool VEC>
-__global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
@@ -504,16 +508,33 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
       for (int e = 0; e < 4; ++e) x[e] = i + e < p.vocab ? __ldg(row + i + e) : 0.0f;
     }
   };
-  // the residual's masses of values i .. i + 3 of node `cur`
-  auto masses = [&](int cur, const Residual& r, int i, double (&m)[4]) {
-    float x[4], y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    load4(p.target + (q0 + cur) * p.target_stride, i, x);
-    if (r.b != 0.0) load4(p.draft + (q0 + cur) * p.draft_stride, i, y);
+  // the residual's masses of kVerifyBatch groups of 4 values of row `cur`: lane's
+  // own of the 128 from i0 on, of the next 128, ... (0 from hi on); all loads first
+  auto masses = [&](int cur, const Residual& r, int i0, double (&m)[kVerifyBatch][4]) {
+    float x[kVerifyBatch][4], y[kVerifyBatch][4];
+    const float* prow = p.target + (q0 + cur) * p.target_stride;
+    const float* qrow = p.draft + (q0 + cur) * p.draft_stride;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) m[e] = mass_of(x[e], y[e], r.a, r.b);
-    for (int g = 0; g < r.gone; ++g) {
-      const int t = s_gone[g] - i;
-      if (t >= 0 && t < 4) m[t == 0 ? 0 : t == 1 ? 1 : t == 2 ? 2 : 3] = 0.0;
+    for (int u = 0; u < kVerifyBatch; ++u) {
+      const int i = i0 + u * 128 + lane * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[u][e] = y[u][e] = 0.0f;
+      if (i < hi) {
+        load4(prow, i, x[u]);
+        if (r.b != 0.0) load4(qrow, i, y[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kVerifyBatch; ++u) {
+      const int i = i0 + u * 128 + lane * 4;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[u][e] = mass_of(x[u][e], y[u][e], r.a, r.b);
+      for (int g = 0; g < r.gone; ++g) {
+        const int t = s_gone[g] - i;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t == e) m[u][e] = 0.0;
+      }
     }
   };
   int turn = 0;
@@ -521,10 +542,11 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
   // CTA and s_rank[which] the CTAs'
   auto total_mass = [&](int cur, const Residual& r, int* which) {
     double acc = 0.0;
-    for (int i = lo + lane * 4; i < hi; i += 128) {
-      double m[4];
-      masses(cur, r, i, m);
-      acc += (m[0] + m[1]) + (m[2] + m[3]);
+    for (int i0 = lo; i0 < hi; i0 += 128 * kVerifyBatch) {
+      double m[kVerifyBatch][4];
+      masses(cur, r, i0, m);
+#pragma unroll
+      for (int u = 0; u < kVerifyBatch; ++u) acc += (m[u][0] + m[u][1]) + (m[u][2] + m[u][3]);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFullMask, acc, o);
@@ -633,31 +655,30 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_draft_kernel(const Veri
       if (warp == aw) {
         double run = w_before;
         int last_pos = -1;
-        for (int i0 = lo; i0 < hi && chosen < 0; i0 += 128) {
-          const int i = i0 + lane * 4;
-          double m[4] = {0.0, 0.0, 0.0, 0.0};
-          if (i < hi) masses(cur, r, i, m);
-          const double c0 = m[0], c1 = c0 + m[1], c2 = c1 + m[2], c3 = c2 + m[3];
-          double incl = c3;
+        for (int i0 = lo; i0 < hi && chosen < 0; i0 += 128 * kVerifyBatch) {
+          double mm[kVerifyBatch][4];
+          masses(cur, r, i0, mm);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double t = __shfl_up_sync(kFullMask, incl, o);
-            if (lane >= o) incl += t;
+          for (int u = 0; u < kVerifyBatch; ++u) {
+            const int i = i0 + u * 128 + lane * 4;
+            const double(&m)[4] = mm[u];
+            const double c0 = m[0], c1 = c0 + m[1], c2 = c1 + m[2], c3 = c2 + m[3];
+            double incl = c3;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const double t = __shfl_up_sync(kFullMask, incl, o);
+              if (lane >= o) incl += t;
+            }
+            const double b = run + (incl - c3);
+            const int hit = m[0] > 0.0 && b + c0 > want ? 0 : m[1] > 0.0 && b + c1 > want ? 1
+                            : m[2] > 0.0 && b + c2 > want ? 2 : m[3] > 0.0 && b + c3 > want ? 3 : 4;
+            const int lastp = m[3] > 0.0 ? 3 : m[2] > 0.0 ? 2 : m[1] > 0.0 ? 1 : m[0] > 0.0 ? 0 : -1;
+            const unsigned hits = __ballot_sync(kFullMask, hit < 4);
+            const unsigned pos = __ballot_sync(kFullMask, lastp >= 0);
+            if (chosen < 0 && hits) chosen = __shfl_sync(kFullMask, i + hit, __ffs(hits) - 1);
+            if (pos) last_pos = __shfl_sync(kFullMask, i + lastp, 31 - __clz(pos));
+            run += __shfl_sync(kFullMask, incl, 31);
           }
-          const double b = run + (incl - c3);
-          const int hit = m[0] > 0.0 && b + c0 > want ? 0 : m[1] > 0.0 && b + c1 > want ? 1
-                          : m[2] > 0.0 && b + c2 > want ? 2 : m[3] > 0.0 && b + c3 > want ? 3 : 4;
-          const int lastp = m[3] > 0.0 ? 3 : m[2] > 0.0 ? 2 : m[1] > 0.0 ? 1 : m[0] > 0.0 ? 0 : -1;
-          const unsigned hits = __ballot_sync(kFullMask, hit < 4);
-          const unsigned pos = __ballot_sync(kFullMask, lastp >= 0);
-          if (hits) {
-            const int src = __ffs(hits) - 1;
-            chosen = __shfl_sync(kFullMask, i + hit, src);
-          } else if (pos) {
-            const int src = 31 - __clz(pos);
-            last_pos = __shfl_sync(kFullMask, i + lastp, src);
-          }
-          run += __shfl_sync(kFullMask, incl, 31);
         }
         if (chosen < 0) chosen = last_pos;
         if (lane == 0) out_tokens[len - 1] = chosen;
@@ -701,9 +722,9 @@ cudaError_t launch_verify_draft(const VerifyShape& sh, int32_t* out_tokens, int3
   cudaError_t e = device_error_word(&p.err);
   if (e != cudaSuccess) return e;
   // CTAs per sequence: as many (up to the portable 8) as keep the launch within
-  // about two waves of resident CTAs and leave each a few thousand values
+  // one wave of resident CTAs (two an SM) and leave each a few thousand values
   int ranks = 1;
-  while (ranks < 8 && sh.num_seqs * ranks < 148 * 4 && sh.vocab / ranks > 4096) ranks *= 2;
+  while (ranks < 8 && sh.num_seqs * ranks <= 148 && sh.vocab / ranks > 4096) ranks *= 2;
   auto vec_ok = [](const float* x, int64_t stride) {
     return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && stride % 4 == 0;
   };

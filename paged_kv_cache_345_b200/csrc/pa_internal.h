@@ -153,7 +153,7 @@ struct TreeShape {
 };
 // Byte offsets of the regions of a pa_decode_tree workspace.
 struct TreeWorkspace {
-  size_t m_off, l_off, acc_off, total;
+  size_t ml_off, acc_off, total;
   int slots;      // partial results (two a CTA)
   int slot_rows;  // rows of one
 };

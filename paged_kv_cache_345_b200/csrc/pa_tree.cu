@@ -55,10 +55,11 @@ constexpr int kTreeKeys = 64;    // keys per tile
 constexpr int kTreeRows = 128;   // rows per query tile
 constexpr int kTreeMinUnits = 2; // least units a CTA takes
 
-// What one partial result belongs to: item `item` (KV head * items + item of
-// rows) of sequence s, split over CTAs first .. last; first < 0: none.
+// What one partial result belongs to: rows [0, rows) of an item, whose first
+// output row is out_row, split over CTAs first .. last; first < 0: none.
 struct TreeHeader {
-  int s, h, row_item, first, last, pad[3];
+  int64_t out_row;
+  int rows, first, last, pad[3];
 };
 
 struct TreeParams {
@@ -69,8 +70,7 @@ struct TreeParams {
   const int32_t* parents;
   unsigned* err;
   TreeHeader* hdr;  // [CTAs][2]
-  float* ws_m;      // [CTAs][2][slot_rows]
-  float* ws_l;
+  float2* ws_ml;    // [CTAs][2][slot_rows]: reference maximum, sum
   float* ws_acc;    // [CTAs][2][D / 4][slot_rows][4]
   int num_heads, num_kv_heads, lg_group, block_size, log2_block_size, num_blocks;
   int max_blocks_per_seq, num_seqs, total_q, max_query_len, slot_rows;
@@ -352,7 +352,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
     RingPos pos{0, 0};
     uint32_t qph = 0;
     int it = 0;  // tiles so far, over all runs
+    bool ended = false;
     runs([&](const TreeRun& r) {
+      ended = false;
       if (!wait_all(bar(kQFull), qph)) return false;
       qph ^= 1;
       for (int t = r.t0; t < r.t1; ++t, ++it) {
@@ -380,8 +382,20 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
         __syncwarp();
         pos.step2<NG>();
       }
+      ended = true;
       return true;
     });
+    // The CTA must not leave while a commit is still to arrive on its barriers:
+    // the queue of the tensor pipe, shared with the SM's other CTA, may hold one
+    // back past the last output. The S, P V and Q barriers' last phases are
+    // waited for by their readers; the last of each granule's and of Q's
+    // "empty" have no reader left, so they are waited for here.
+    if (ended) {
+      const int uses = (2 * it - lane + NG - 1) / NG;  // of granule `lane`
+      if (lane < NG && 2 * it > lane) mbar_wait(bar(kEmpty + lane), (uses - 1) & 1, p.err);
+      mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
+      __syncwarp();
+    }
   } else if (warp == 3) {
     // ------------------------------------------------------------ P V MMAs
     constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
@@ -439,10 +453,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
         float alpha = 1.0f;
         uint32_t pw[KEYN / 2];
         if (warp_real) {
-          uint32_t sv[2][32];
-          tc::ld32(t_s(x, it & 1) + lane_off, sv[0]);
-          tc::ld32(t_s(x, it & 1) + lane_off + 32, sv[1]);
-          tc::wait_ld();
+          uint32_t sv[KEYN];
+          tc::ld64_wait(t_s(x, it & 1) + lane_off, sv);
           if (key0 + KEYN > before) {
             // bit i: key key0 + i is seen. Keys before the step, then the row's
             // own and its ancestors' (a parent comes before its child).
@@ -471,14 +483,12 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
               const uint32_t bits = static_cast<uint32_t>(seen >> (32 * c));
 #pragma unroll
               for (int i = 0; i < 32; ++i)
-                if (!((bits >> i) & 1)) sv[c][i] = 0xff800000u;  // -inf
+                if (!((bits >> i) & 1)) sv[32 * c + i] = 0xff800000u;  // -inf
             }
           }
           float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sv[c][i]));
+          for (int i = 0; i < KEYN; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sv[i]));
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs;
           const bool move = mx > m_use + 8.0f;
           const float m_new = move ? mx : m_use;
@@ -488,9 +498,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
           float rs0 = 0.0f, rs1 = 0.0f;
 #pragma unroll
           for (int e = 0; e < KEYN / 2; ++e) {
-            const int i0 = 2 * e;
-            const float a = exp2_fast(fmaf(__uint_as_float(sv[i0 >> 5][i0 & 31]), qs, -m_sub));
-            const float b = exp2_fast(fmaf(__uint_as_float(sv[(i0 + 1) >> 5][(i0 + 1) & 31]), qs, -m_sub));
+            const float a = exp2_fast(fmaf(__uint_as_float(sv[2 * e]), qs, -m_sub));
+            const float b = exp2_fast(fmaf(__uint_as_float(sv[2 * e + 1]), qs, -m_sub));
             pw[e] = pack_bf16x2(a, b);
             rs0 += __uint_as_float(pw[e] << 16);
             rs1 += __uint_as_float(pw[e] & 0xffff0000u);
@@ -505,13 +514,13 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t ov[32];
-            tc::ld32(t_o(x) + lane_off + c * 32, ov);
-            tc::wait_ld();
+            tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
 #pragma unroll
             for (int i = 0; i < 32; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * alpha);
             tc::st32(t_o(x) + lane_off + c * 32, ov);
           }
         }
+        __syncwarp();  // (lanes parted over their ancestors; the store is the warp's)
         if (warp_real) {
           tc::st32(t_s(x, it & 1) + lane_off, pw);
           tc::wait_st();
@@ -550,8 +559,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];
-          tc::ld32(t_o(x) + lane_off + c * 32, ov);
-          tc::wait_ld();
+          tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
           if (real) {
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
@@ -570,15 +578,13 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
         const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + side;
         const int row = x * kTreeRows + r_;
         if (real) {
-          p.ws_m[slot * p.slot_rows + row] = m_use;
-          p.ws_l[slot * p.slot_rows + row] = l_run;
+          p.ws_ml[slot * p.slot_rows + row] = make_float2(m_use, l_run);
         }
         float* dst = p.ws_acc + (slot * D * p.slot_rows) + row * 4;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           uint32_t ov[32];
-          tc::ld32(t_o(x) + lane_off + c * 32, ov);
-          tc::wait_ld();
+          tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
           if (real) {
 #pragma unroll
             for (int v = 0; v < 8; ++v)
@@ -588,9 +594,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
         }
         if (teller) {
           TreeHeader hd{};
-          hd.s = r.s;
-          hd.h = r.h;
-          hd.row_item = r.row_item;
+          const int tok0 = r.row_item * item_tokens;
+          hd.out_row = (static_cast<int64_t>(r.q0) + tok0) * p.num_heads + (r.h << p.lg_group);
+          hd.rows = min(item_tokens, r.n - tok0) << p.lg_group;
           hd.first = static_cast<int>(r.item_unit / share);
           hd.last = static_cast<int>((r.item_unit + r.nt - 1) / share);
           hdr[side] = hd;
@@ -608,11 +614,14 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
 }
 
 // Merge of the items that were split: the CTAs that held a part of one share
-// its columns (in fours), each thread one row of four columns over all parts in
-// key order:
-//   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j.
+// its pieces of 32 rows x 4 columns, a warp each, a lane one row:
+//   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j
+// over all parts in key order. Latency-bound (a header, then one round trip per
+// kMergeParts parts, kMergePieces pieces at once).
+constexpr int kMergeParts = 4, kMergePieces = 2, kMergeWarps = 8;
+
 template <int D>
-__global__ void __launch_bounds__(512) tree_merge_kernel(const TreeParams p, int query_tiles) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) tree_merge_kernel(const TreeParams p) {
   pdl_wait();
   pdl_launch_dependents();
   const int slot = blockIdx.x, cta = slot >> 1;
@@ -620,59 +629,69 @@ __global__ void __launch_bounds__(512) tree_merge_kernel(const TreeParams p, int
   if (hd.first < 0) return;
   const int rank = cta - hd.first, parts = hd.last - hd.first + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = 1 << p.lg_group;
-  const int q0 = __ldg(p.query_start + hd.s), n = __ldg(p.query_start + hd.s + 1) - q0;
-  const int tok0 = hd.row_item * query_tiles * (kTreeRows >> p.lg_group);
-  const int rows = min(query_tiles * kTreeRows, (n - tok0) * G);
-  const int groups = (rows + 31) / 32;               // of 32 rows
-  const int cols = (D / 4 - rank + parts - 1) / parts;  // this CTA's columns: rank, rank + parts, ...
-  for (int w = warp; w < groups * cols; w += 16) {
-    const int row = (w % groups) * 32 + lane, col = rank + (w / groups) * parts;
-    if (row >= rows) continue;
-    float M = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int B = 8;
-    for (int j0 = 0; j0 < parts; j0 += B) {
-      float mq[B], lq[B];
-      float4 vq[B];
+  const int groups = (hd.rows + 31) / 32, pieces = groups * (D / 4);
+  // the first part lies in its CTA's second slot, the others in the first
+  auto slot_of = [&](int j) { return 2 * static_cast<int64_t>(hd.first + j) + (j == 0 ? 1 : 0); };
+  for (int w0 = rank + warp * parts; w0 < pieces; w0 += kMergePieces * kMergeWarps * parts) {
+    int row[kMergePieces], col[kMergePieces];
+    bool on[kMergePieces];
+    float M[kMergePieces], l[kMergePieces], acc[kMergePieces][4];
 #pragma unroll
-      for (int j = 0; j < B; ++j) {  // (a place past the last part loads that part again)
-        const int k = min(j0 + j, parts - 1);
-        // the first part lies in its CTA's second slot, the others in the first
-        const int64_t sl = 2 * static_cast<int64_t>(hd.first + k) + (k == 0 ? 1 : 0);
-        mq[j] = ld_cg_f32(p.ws_m + sl * p.slot_rows + row);
-        lq[j] = ld_cg_f32(p.ws_l + sl * p.slot_rows + row);
-        vq[j] = ld_cg_f32x4(p.ws_acc + (sl * (D / 4) + col) * p.slot_rows * 4 + row * 4);
-      }
-      float bm = M;
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        if (j0 + j >= parts) mq[j] = -INFINITY;
-        bm = fmaxf(bm, mq[j]);
-      }
-      if (bm == -INFINITY) continue;  // this row saw no key in these parts
-      const float sc = exp2f(M - bm);
-      l *= sc;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] *= sc;
-#pragma unroll
-      for (int j = 0; j < B; ++j) {
-        // (a part without a key for this row may hold 0 * stale sums: left out)
-        if (mq[j] == -INFINITY) continue;
-        const float wt = exp2f(mq[j] - bm);
-        l = fmaf(wt, lq[j], l);
-        acc[0] = fmaf(wt, vq[j].x, acc[0]);
-        acc[1] = fmaf(wt, vq[j].y, acc[1]);
-        acc[2] = fmaf(wt, vq[j].z, acc[2]);
-        acc[3] = fmaf(wt, vq[j].w, acc[3]);
-      }
-      M = bm;
+    for (int e = 0; e < kMergePieces; ++e) {
+      const int w = w0 + e * kMergeWarps * parts;
+      row[e] = (w % groups) * 32 + lane;
+      col[e] = w / groups;
+      on[e] = w < pieces && row[e] < hd.rows;
+      M[e] = -INFINITY;
+      l[e] = acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.0f;
     }
-    const float inv = 1.0f / l;
-    const int tok = tok0 + (row >> p.lg_group);
-    __nv_bfloat16* dst = p.out + ((static_cast<int64_t>(q0) + tok) * p.num_heads +
-                                  (hd.h << p.lg_group) + (row & (G - 1))) * D + col * 4;
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    for (int j0 = 0; j0 < parts; j0 += kMergeParts) {
+      float2 ml[kMergePieces][kMergeParts];
+      float4 v[kMergePieces][kMergeParts];
+#pragma unroll
+      for (int e = 0; e < kMergePieces; ++e)
+#pragma unroll
+        for (int j = 0; j < kMergeParts; ++j) {
+          ml[e][j] = make_float2(-INFINITY, 0.0f);
+          if (on[e] && j0 + j < parts) {
+            const int64_t sl = slot_of(j0 + j);
+            ml[e][j] = ld_cg_f32x2(reinterpret_cast<const float*>(p.ws_ml + sl * p.slot_rows + row[e]));
+            v[e][j] = ld_cg_f32x4(p.ws_acc + ((sl * (D / 4) + col[e]) * p.slot_rows + row[e]) * 4);
+          }
+        }
+#pragma unroll
+      for (int e = 0; e < kMergePieces; ++e) {
+        float bm = M[e];
+#pragma unroll
+        for (int j = 0; j < kMergeParts; ++j) bm = fmaxf(bm, ml[e][j].x);
+        if (bm == -INFINITY) continue;  // this row saw no key in these parts
+        const float sc = exp2f(M[e] - bm);
+        l[e] *= sc;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[e][i] *= sc;
+#pragma unroll
+        for (int j = 0; j < kMergeParts; ++j) {
+          if (ml[e][j].x == -INFINITY) continue;  // (no part, or none of its keys seen)
+          const float wt = exp2f(ml[e][j].x - bm);
+          l[e] = fmaf(wt, ml[e][j].y, l[e]);
+          acc[e][0] = fmaf(wt, v[e][j].x, acc[e][0]);
+          acc[e][1] = fmaf(wt, v[e][j].y, acc[e][1]);
+          acc[e][2] = fmaf(wt, v[e][j].z, acc[e][2]);
+          acc[e][3] = fmaf(wt, v[e][j].w, acc[e][3]);
+        }
+        M[e] = bm;
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < kMergePieces; ++e) {
+      if (!on[e]) continue;
+      const float inv = 1.0f / l[e];
+      const int64_t out = hd.out_row + static_cast<int64_t>(row[e] >> p.lg_group) * p.num_heads +
+                          (row[e] & ((1 << p.lg_group) - 1));
+      *reinterpret_cast<uint2*>(p.out + out * D + col[e] * 4) =
+          make_uint2(pack_bf16x2(acc[e][0] * inv, acc[e][1] * inv),
+                     pack_bf16x2(acc[e][2] * inv, acc[e][3] * inv));
+    }
   }
 }
 
@@ -726,7 +745,7 @@ cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* 
   e = launch_pdl(pa_tree_kernel<D, QT>, dim3(ctas), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
                  qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_merge_kernel<D>, dim3(2 * ctas), dim3(512), 0, stream, p, QT);
+  return launch_pdl(tree_merge_kernel<D>, dim3(2 * ctas), dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 }  // namespace
@@ -747,9 +766,8 @@ TreeWorkspace tree_workspace(int num_heads, int num_kv_heads, int head_dim, int 
   w.slot_rows = qt == 2 ? 2 * kTreeRows : static_cast<int>((rows + 31) / 32 * 32);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t each = static_cast<size_t>(w.slots) * w.slot_rows;
-  w.m_off = up(static_cast<size_t>(2 * tree_ctas(1)) * sizeof(TreeHeader));
-  w.l_off = w.m_off + up(each * sizeof(float));
-  w.acc_off = w.l_off + up(each * sizeof(float));
+  w.ml_off = up(static_cast<size_t>(2 * tree_ctas(1)) * sizeof(TreeHeader));
+  w.acc_off = w.ml_off + up(each * sizeof(float2));
   w.total = w.acc_off + each * head_dim * sizeof(float);
   return w;
 }
@@ -770,8 +788,7 @@ cudaError_t launch_decode_tree(const TreeShape& sh, void* out, const void* q, co
   cudaError_t e = device_error_word(&p.err);
   if (e != cudaSuccess) return e;
   p.hdr = reinterpret_cast<TreeHeader*>(ws);
-  p.ws_m = reinterpret_cast<float*>(ws + w.m_off);
-  p.ws_l = reinterpret_cast<float*>(ws + w.l_off);
+  p.ws_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   p.ws_acc = reinterpret_cast<float*>(ws + w.acc_off);
   p.num_heads = sh.num_heads;
   p.num_kv_heads = sh.num_kv_heads;
