@@ -133,38 +133,39 @@ __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq
   return static_cast<int64_t>(t.nt) * t.items * p.num_kv_heads;
 }
 
-// One run of key tiles of one item.
+// One run of key tiles of one item. Units count from the CTA's first (a
+// sequence's own fit 31 bits: checked on the host for the longest).
 struct TreeRun {
   int s, q0, n, L, nt, h, row_item, t0, t1;
-  int64_t item_unit;  // the item's first unit
+  int item_unit;  // the item's first unit
 };
 
-// Calls f(run) for each run of the units [u0, u1), from sequence s on, whose
-// units start at `base`; stops when f returns false.
+// Calls f(run) for each run of the units [0, units), from sequence s on, whose
+// first unit is `base` (<= 0); stops when f returns false.
 template <typename F>
-__device__ __forceinline__ void tree_runs(const TreeParams& p, int64_t u0, int64_t u1, int s,
-                                          int64_t base, int item_tokens, F&& f) {
-  int64_t u = u0;
-  while (u < u1 && s < p.num_seqs) {
+__device__ __forceinline__ void tree_runs(const TreeParams& p, int units, int s, int base,
+                                          int item_tokens, F&& f) {
+  int u = 0;
+  while (u < units && s < p.num_seqs) {
     const TreeSeq t = tree_seq(p, s, item_tokens);
-    const int64_t units = tree_units(p, t);
-    while (u < u1 && u - base < units) {
-      const int64_t item = (u - base) / t.nt;
+    const int own = t.nt * t.items * p.num_kv_heads;
+    while (u < units && u - base < own) {
+      const unsigned item = static_cast<unsigned>(u - base) / static_cast<unsigned>(t.nt);
       TreeRun r;
       r.s = s;
       r.q0 = t.q0;
       r.n = t.n;
       r.L = t.L;
       r.nt = t.nt;
-      r.h = static_cast<int>(item / t.items);
-      r.row_item = static_cast<int>(item - static_cast<int64_t>(r.h) * t.items);
-      r.item_unit = base + item * t.nt;
-      r.t0 = static_cast<int>(u - r.item_unit);
-      r.t1 = static_cast<int>(min(static_cast<int64_t>(t.nt), r.t0 + (u1 - u)));
+      r.h = t.items == 1 ? item : item / static_cast<unsigned>(t.items);
+      r.row_item = static_cast<int>(item) - r.h * t.items;
+      r.item_unit = base + static_cast<int>(item) * t.nt;
+      r.t0 = u - r.item_unit;
+      r.t1 = min(t.nt, r.t0 + (units - u));
       if (!f(r)) return;
       u += r.t1 - r.t0;
     }
-    base += units;
+    base += own;
     ++s;
   }
 }
@@ -198,9 +199,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
   constexpr int kFull = 0, kEmpty = NG, kQFull = 2 * NG, kQEmpty = 2 * NG + 1, kS = 2 * NG + 2;
   constexpr int kP = kS + 2 * QT, kO = kP + 2 * QT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::kScratch);
-  int64_t* s_sum = reinterpret_cast<int64_t*>(sm + Cfg::kScratch + 16);  // [12] per warp, then total
-  int64_t* s_base = s_sum + 13;
-  int* s_seq = reinterpret_cast<int*>(s_sum + 14);
+  int64_t* s_sum = reinterpret_cast<int64_t*>(sm + Cfg::kScratch + 16);  // [12]: one a warp
+  int* s_base = reinterpret_cast<int*>(s_sum + 13);
+  int* s_seq = s_base + 1;
   auto q_s = [&](int x) { return smem_u32(sm + x * Cfg::kQBytes); };
   auto gran = [&](int st) { return smem_u32(sm + Cfg::kRing) + st * Cfg::kGran; };
 
@@ -237,52 +238,49 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
   pdl_wait();  // inputs may come from the previous kernel in the stream
   pdl_launch_dependents();
 
-  // The units of the batch, then this CTA's run and the sequence it starts in.
-  // Scans of kThreads sequences at a time, each thread one.
+  // The units of the batch, then this CTA's run and the sequence it starts in:
+  // each thread sums its own consecutive sequences, one scan joins the threads,
+  // and the thread whose sequences hold the first unit finds the one.
   constexpr int NT = Cfg::kThreads, NW = NT / 32;
-  int64_t total = 0;
-  for (int s0 = 0; s0 < p.num_seqs; s0 += NT) {
-    const int s = s0 + threadIdx.x;
-    if (s < p.num_seqs) {
-      const TreeSeq t = tree_seq(p, s, item_tokens);
-      if (t.bad && blockIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT);
-      total += tree_units(p, t);
-    }
+  const int per = (p.num_seqs + NT - 1) / NT;
+  const int sa = threadIdx.x * per, sb = min(sa + per, p.num_seqs);
+  int64_t own = 0;
+#pragma unroll 4
+  for (int s = sa; s < sb; ++s) {
+    const TreeSeq t = tree_seq(p, s, item_tokens);
+    if (t.bad && blockIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT);
+    own += tree_units(p, t);
   }
+  int64_t incl = own;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFullMask, total, o);
-  if (lane == 0) s_sum[warp] = total;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(kFullMask, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_sum[warp] = incl;
   if (threadIdx.x == 0) *s_seq = p.num_seqs;
   __syncthreads();
-  total = 0;
-  for (int w = 0; w < NW; ++w) total += s_sum[w];
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const int64_t v = s_sum[w];
+    if (w < warp) incl += v;
+    total += v;
+  }
   int64_t share = (total + gridDim.x - 1) / gridDim.x;
   if (share < kTreeMinUnits) share = kTreeMinUnits;
-  const int64_t u0 = blockIdx.x * share, u1 = min(u0 + share, total);
-  if (u0 < u1) {
-    int64_t before = 0;
-    for (int s0 = 0; s0 < p.num_seqs && before <= u0; s0 += NT) {
-      const int s = s0 + threadIdx.x;
-      const int64_t mine = s < p.num_seqs ? tree_units(p, tree_seq(p, s, item_tokens)) : 0;
-      int64_t incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(kFullMask, incl, o);
-        if (lane >= o) incl += v;
-      }
-      __syncthreads();
-      if (lane == 31) s_sum[warp] = incl;
-      __syncthreads();
-      int64_t chunk = 0;
-      for (int w = 0; w < NW; ++w) {
-        if (w < warp) incl += s_sum[w];
-        chunk += s_sum[w];
-      }
-      if (before + incl - mine <= u0 && u0 < before + incl) {
+  const int64_t u0 = blockIdx.x * share;
+  const int units = static_cast<int>(max(static_cast<int64_t>(0), min(share, total - u0)));
+  if (units > 0 && incl - own <= u0 && u0 < incl) {
+    int64_t at = incl - own;
+    for (int s = sa; s < sb; ++s) {
+      const int64_t n = tree_units(p, tree_seq(p, s, item_tokens));
+      if (u0 < at + n) {
         *s_seq = s;
-        *s_base = before + incl - mine;
+        *s_base = static_cast<int>(at - u0);
+        break;
       }
-      before += chunk;
+      at += n;
     }
   }
   tc::fence_before_sync();
@@ -290,11 +288,11 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const int seq0 = *s_seq;
-  const int64_t base0 = *s_base;
+  const int base0 = *s_base;
   auto t_s = [&](int x, int b) { return tmem + (2 * x + b) * KEYN; };
   auto t_o = [&](int x) { return tmem + 2 * QT * KEYN + x * D; };
   auto runs = [&](auto&& f) {
-    if (u0 < u1) tree_runs(p, u0, u1, seq0, base0, item_tokens, f);
+    if (units > 0) tree_runs(p, units, seq0, base0, item_tokens, f);
   };
 
   if (warp < 2) {
@@ -445,6 +443,10 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
       // (warps without a row compute nothing, but take part in every barrier)
       const bool warp_real = (r.row_item * item_tokens + x * TOK + ((wq * 32) >> p.lg_group)) < r.n;
       const int before = r.L - r.n;  // tokens every row sees
+      // the row's parent, read here so that it (and its line) is there for the
+      // tiles of the step's own rows
+      int parent = -1;
+      if (p.parents != nullptr && real) parent = __ldg(p.parents + r.q0 + my_tok);
       float m_use = -INFINITY, l_run = 0.0f;
       for (int t = r.t0; t < r.t1; ++t, ++it) {
         if (!wait_all(bar(kS + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
@@ -466,15 +468,16 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
                 if (top >= 63) seen = ~0ull;
                 else if (top >= 0) seen |= (2ull << top) - 1;
               } else {
-                int a = my_tok;
-                while (a >= 0 && a >= rel) {
+                int a = my_tok, up = parent;
+                while (a >= rel) {
                   if (a - rel < 64) seen |= 1ull << (a - rel);
-                  const int up = __ldg(p.parents + r.q0 + a);
                   if (up >= a || up < -1) {
                     atomicOr(p.err, PA_DEVERR_DRAFT);
                     break;
                   }
                   a = up;
+                  if (a < 0) break;
+                  up = __ldg(p.parents + r.q0 + a);
                 }
               }
             }
@@ -554,21 +557,60 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
       if (!warp_real) return true;
       if (r.t0 == 0 && r.t1 == r.nt) {
         const float inv = 1.0f / l_run;
-        __nv_bfloat16* dst =
-            p.out + ((static_cast<int64_t>(r.q0) + my_tok) * p.num_heads + (r.h << p.lg_group) + g) * D;
+        // row r_ of the item is output row base + (r_ >> lg_group) * num_heads + its head
+        const int64_t base = (static_cast<int64_t>(r.q0) + r.row_item * item_tokens + x * TOK) * p.num_heads +
+                             (r.h << p.lg_group);
+        if (QT == 1 && p.slot_rows <= 64) {
+          // Q's rows 64 .. 127 hold nothing: 32 rows a warp pass through there (16-byte
+          // pieces swizzled by row), so that the stores are whole rows
+          const uint32_t half0 = q_s(0) + 64 * 128;
+          auto piece = [&](int row, int c) {  // of this warp's 32 rows
+            const int o = (wq * 32 + row) * D * 2 + ((c ^ (row & 7)) << 4);
+            return half0 + (o >> 13) * Cfg::kQHalf + (o & 8191);
+          };
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t ov[32];
-          tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
-          if (real) {
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              uint4 w;
-              w.x = pack_bf16x2(__uint_as_float(ov[8 * v]) * inv, __uint_as_float(ov[8 * v + 1]) * inv);
-              w.y = pack_bf16x2(__uint_as_float(ov[8 * v + 2]) * inv, __uint_as_float(ov[8 * v + 3]) * inv);
-              w.z = pack_bf16x2(__uint_as_float(ov[8 * v + 4]) * inv, __uint_as_float(ov[8 * v + 5]) * inv);
-              w.w = pack_bf16x2(__uint_as_float(ov[8 * v + 6]) * inv, __uint_as_float(ov[8 * v + 7]) * inv);
-              *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = w;
+              const uint32_t w0 = pack_bf16x2(__uint_as_float(ov[8 * v]) * inv, __uint_as_float(ov[8 * v + 1]) * inv);
+              const uint32_t w1 = pack_bf16x2(__uint_as_float(ov[8 * v + 2]) * inv, __uint_as_float(ov[8 * v + 3]) * inv);
+              const uint32_t w2 = pack_bf16x2(__uint_as_float(ov[8 * v + 4]) * inv, __uint_as_float(ov[8 * v + 5]) * inv);
+              const uint32_t w3 = pack_bf16x2(__uint_as_float(ov[8 * v + 6]) * inv, __uint_as_float(ov[8 * v + 7]) * inv);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, c * 4 + v)),
+                           "r"(w0), "r"(w1), "r"(w2), "r"(w3)
+                           : "memory");
+            }
+          }
+          __syncwarp();
+          constexpr int kPieces = D / 8, kPer = 32 / kPieces;  // 16-byte pieces a row, rows a store
+          const int left = (r.n - r.row_item * item_tokens) << p.lg_group;  // rows of the item from here on
+#pragma unroll
+          for (int i = 0; i < 32 / kPer; ++i) {
+            const int row = i * kPer + lane / kPieces, c = lane % kPieces, rr = wq * 32 + row;
+            const uint4 w = lds128(piece(row, c));
+            if (rr < left)
+              *reinterpret_cast<uint4*>(p.out + (base + static_cast<int64_t>(rr >> p.lg_group) * p.num_heads +
+                                                 (rr & (G - 1))) * D + c * 8) = w;
+          }
+          __syncwarp();
+        } else {
+          __nv_bfloat16* dst = p.out + (base + static_cast<int64_t>(tok) * p.num_heads + g) * D;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t ov[32];
+            tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
+            if (real) {
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                uint4 w;
+                w.x = pack_bf16x2(__uint_as_float(ov[8 * v]) * inv, __uint_as_float(ov[8 * v + 1]) * inv);
+                w.y = pack_bf16x2(__uint_as_float(ov[8 * v + 2]) * inv, __uint_as_float(ov[8 * v + 3]) * inv);
+                w.z = pack_bf16x2(__uint_as_float(ov[8 * v + 4]) * inv, __uint_as_float(ov[8 * v + 5]) * inv);
+                w.w = pack_bf16x2(__uint_as_float(ov[8 * v + 6]) * inv, __uint_as_float(ov[8 * v + 7]) * inv);
+                *reinterpret_cast<uint4*>(dst + c * 32 + v * 8) = w;
+              }
             }
           }
         }
@@ -597,8 +639,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
           const int tok0 = r.row_item * item_tokens;
           hd.out_row = (static_cast<int64_t>(r.q0) + tok0) * p.num_heads + (r.h << p.lg_group);
           hd.rows = min(item_tokens, r.n - tok0) << p.lg_group;
-          hd.first = static_cast<int>(r.item_unit / share);
-          hd.last = static_cast<int>((r.item_unit + r.nt - 1) / share);
+          hd.first = static_cast<int>((u0 + r.item_unit) / share);
+          hd.last = static_cast<int>((u0 + r.item_unit + r.nt - 1) / share);
           hdr[side] = hd;
         }
       }
@@ -613,15 +655,19 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
   if (warp == 2) tc::tmem_dealloc(tmem, Cfg::kTmemCols);
 }
 
-// Merge of the items that were split: the CTAs that held a part of one share
-// its pieces of 32 rows x 4 columns, a warp each, a lane one row:
+// Merge of the items that were split:
 //   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j
-// over all parts in key order. Latency-bound (a header, then one round trip per
-// kMergeParts parts, kMergePieces pieces at once).
-constexpr int kMergeParts = 4, kMergePieces = 2, kMergeWarps = 8;
+// over all parts j. An item's pieces (32 rows x 4 columns, a lane one row) are
+// dealt to the CTAs that held a part of it. With fewer pieces than warps, W warps
+// share a piece, taking the parts in turn and joining in shared memory in their
+// order; so the sums' order goes by the item's rows and parts alone.
+// Latency-bound: a header, one round trip per kMergeParts W parts.
+constexpr int kMergeParts = 7, kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32, 4) tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const TreeParams p) {
+  __shared__ float s_m[kMergeWarps][32], s_l[kMergeWarps][32];
+  __shared__ float4 s_acc[kMergeWarps][32];
   pdl_wait();
   pdl_launch_dependents();
   const int slot = blockIdx.x, cta = slot >> 1;
@@ -629,69 +675,82 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) tree_merge_kernel(const T
   if (hd.first < 0) return;
   const int rank = cta - hd.first, parts = hd.last - hd.first + 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (hd.rows + 31) / 32, pieces = groups * (D / 4);
-  // the first part lies in its CTA's second slot, the others in the first
-  auto slot_of = [&](int j) { return 2 * static_cast<int64_t>(hd.first + j) + (j == 0 ? 1 : 0); };
-  for (int w0 = rank + warp * parts; w0 < pieces; w0 += kMergePieces * kMergeWarps * parts) {
-    int row[kMergePieces], col[kMergePieces];
-    bool on[kMergePieces];
-    float M[kMergePieces], l[kMergePieces], acc[kMergePieces][4];
-#pragma unroll
-    for (int e = 0; e < kMergePieces; ++e) {
-      const int w = w0 + e * kMergeWarps * parts;
-      row[e] = (w % groups) * 32 + lane;
-      col[e] = w / groups;
-      on[e] = w < pieces && row[e] < hd.rows;
-      M[e] = -INFINITY;
-      l[e] = acc[e][0] = acc[e][1] = acc[e][2] = acc[e][3] = 0.0f;
-    }
-    for (int j0 = 0; j0 < parts; j0 += kMergeParts) {
-      float2 ml[kMergePieces][kMergeParts];
-      float4 v[kMergePieces][kMergeParts];
-#pragma unroll
-      for (int e = 0; e < kMergePieces; ++e)
+  const int groups = (hd.rows + 31) >> 5, pieces = groups * (D / 4);
+  const int mine = (pieces - rank + parts - 1) / parts;  // pieces rank, rank + parts, ...
+  if (mine <= 0) return;
+  const int W = mine >= 5 ? 1 : mine >= 3 ? 2 : mine == 2 ? 4 : 8;
+  const int sub = warp & (W - 1);
+  for (int k0 = 0; k0 < mine; k0 += kMergeWarps / W) {
+    const int k = k0 + warp / W;
+    const int w = rank + k * parts;
+    const int row = (w % groups) * 32 + lane, col = w / groups;
+    const bool on = k < mine && row < hd.rows;
+    float M = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (on) {
+      const float* ml = reinterpret_cast<const float*>(p.ws_ml + row);
+      const float* av = p.ws_acc + (static_cast<int64_t>(col) * p.slot_rows + row) * 4;
+      for (int j0 = sub; j0 < parts; j0 += kMergeParts * W) {
+        float2 mq[kMergeParts];
+        float4 v[kMergeParts];
 #pragma unroll
         for (int j = 0; j < kMergeParts; ++j) {
-          ml[e][j] = make_float2(-INFINITY, 0.0f);
-          if (on[e] && j0 + j < parts) {
-            const int64_t sl = slot_of(j0 + j);
-            ml[e][j] = ld_cg_f32x2(reinterpret_cast<const float*>(p.ws_ml + sl * p.slot_rows + row[e]));
-            v[e][j] = ld_cg_f32x4(p.ws_acc + ((sl * (D / 4) + col[e]) * p.slot_rows + row[e]) * 4);
+          const int jj = j0 + j * W;
+          mq[j] = make_float2(-INFINITY, 0.0f);
+          if (jj < parts) {
+            // the first part lies in its CTA's second slot, the others in the first
+            const int64_t sl = 2 * static_cast<int64_t>(hd.first + jj) + (jj == 0 ? 1 : 0);
+            mq[j] = ld_cg_f32x2(ml + sl * p.slot_rows * 2);
+            v[j] = ld_cg_f32x4(av + sl * p.slot_rows * D);
           }
         }
+        float bm = M;
 #pragma unroll
-      for (int e = 0; e < kMergePieces; ++e) {
-        float bm = M[e];
-#pragma unroll
-        for (int j = 0; j < kMergeParts; ++j) bm = fmaxf(bm, ml[e][j].x);
+        for (int j = 0; j < kMergeParts; ++j) bm = fmaxf(bm, mq[j].x);
         if (bm == -INFINITY) continue;  // this row saw no key in these parts
-        const float sc = exp2f(M[e] - bm);
-        l[e] *= sc;
+        const float sc = exp2f(M - bm);
+        l *= sc;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[e][i] *= sc;
+        for (int i = 0; i < 4; ++i) acc[i] *= sc;
 #pragma unroll
         for (int j = 0; j < kMergeParts; ++j) {
-          if (ml[e][j].x == -INFINITY) continue;  // (no part, or none of its keys seen)
-          const float wt = exp2f(ml[e][j].x - bm);
-          l[e] = fmaf(wt, ml[e][j].y, l[e]);
-          acc[e][0] = fmaf(wt, v[e][j].x, acc[e][0]);
-          acc[e][1] = fmaf(wt, v[e][j].y, acc[e][1]);
-          acc[e][2] = fmaf(wt, v[e][j].z, acc[e][2]);
-          acc[e][3] = fmaf(wt, v[e][j].w, acc[e][3]);
+          if (mq[j].x == -INFINITY) continue;  // (no part, or none of its keys seen)
+          const float wt = exp2f(mq[j].x - bm);
+          l = fmaf(wt, mq[j].y, l);
+          acc[0] = fmaf(wt, v[j].x, acc[0]);
+          acc[1] = fmaf(wt, v[j].y, acc[1]);
+          acc[2] = fmaf(wt, v[j].z, acc[2]);
+          acc[3] = fmaf(wt, v[j].w, acc[3]);
         }
-        M[e] = bm;
+        M = bm;
       }
     }
-#pragma unroll
-    for (int e = 0; e < kMergePieces; ++e) {
-      if (!on[e]) continue;
-      const float inv = 1.0f / l[e];
-      const int64_t out = hd.out_row + static_cast<int64_t>(row[e] >> p.lg_group) * p.num_heads +
-                          (row[e] & ((1 << p.lg_group) - 1));
-      *reinterpret_cast<uint2*>(p.out + out * D + col[e] * 4) =
-          make_uint2(pack_bf16x2(acc[e][0] * inv, acc[e][1] * inv),
-                     pack_bf16x2(acc[e][2] * inv, acc[e][3] * inv));
+    if (W > 1) {  // (the same for the whole CTA)
+      __syncthreads();
+      s_m[warp][lane] = M;
+      s_l[warp][lane] = l;
+      s_acc[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      __syncthreads();
+      if (sub != 0) continue;
+      for (int i = 1; i < W; ++i) {
+        const float m2 = s_m[warp + i][lane];
+        if (m2 == -INFINITY) continue;
+        const float bm = fmaxf(M, m2);
+        const float f1 = exp2f(M - bm), f2 = exp2f(m2 - bm);
+        const float4 v = s_acc[warp + i][lane];
+        l = l * f1 + s_l[warp + i][lane] * f2;
+        acc[0] = acc[0] * f1 + v.x * f2;
+        acc[1] = acc[1] * f1 + v.y * f2;
+        acc[2] = acc[2] * f1 + v.z * f2;
+        acc[3] = acc[3] * f1 + v.w * f2;
+        M = bm;
+      }
     }
+    if (!on) continue;
+    const float inv = 1.0f / l;
+    const int64_t out = hd.out_row + static_cast<int64_t>(row >> p.lg_group) * p.num_heads +
+                        (row & ((1 << p.lg_group) - 1));
+    *reinterpret_cast<uint2*>(p.out + out * D + col * 4) =
+        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
   }
 }
 
