@@ -675,7 +675,7 @@ int pa_decode_tree(void* out, const void* q, const void* k_cache, const void* v_
  *                  out_path (0 for a sequence without rows).
  *   target_probs   device, float32, row r at r * target_stride: the target's
  *                  probabilities of the token after row r, [vocab_size]. Rows are
- *                  taken to sum to 1; values not > 0 count as 0.
+ *                  taken to sum to 1; values not > 0 (NaN too) count as 0.
  *   draft_probs    device, float32, likewise with draft_stride: what row r's
  *                  children were sampled from (leaves: not read); or NULL.
  *   draft_tokens   device, int32 [total_q]: each row's token (row 0: not read).

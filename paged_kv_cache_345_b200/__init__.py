@@ -183,18 +183,25 @@ def _check(status: int) -> None:
 
 # ------------------------------------------------------------ tensor helpers
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt == torch.bfloat16:
         return PA_BF16
-    if t.dtype == torch.float32:
+    if dt == torch.float32:
         return PA_F32
-    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
+    if dt in (torch.uint8, torch.float8_e4m3fn):
         return PA_FP8_E4M3
     raise TypeError(f"unsupported dtype {t.dtype} (float32, bfloat16, or uint8 E4M3 codes)")
 
@@ -254,6 +261,25 @@ def _on_device(tensors, stream):
     return torch.cuda.device(dev), _stream(stream, dev)
 
 
+def _call(fn, args, tensors, stream):
+    """fn(*args, stream pointer) on the tensors' device, checked as in _on_device. The
+    usual call, every tensor on the current device, takes a shorter way there."""
+    torch = _torch()
+    if stream is None and torch.cuda.is_initialized():
+        here = torch.cuda.current_device()
+        for t in tensors:
+            if t is not None and t.get_device() != here:
+                break
+        else:
+            status = fn(*args, _stream(None, here))
+            if status != PA_OK:
+                _check(status)
+            return
+    guard, st = _on_device(tensors, stream)
+    with guard:
+        _check(fn(*args, st))
+
+
 # ---------------------------------------------------------------- kernels
 
 def pa_kv_append(k_new, v_new, slot_mapping, k_cache, v_cache, stream=None) -> None:
@@ -265,13 +291,11 @@ def pa_kv_append(k_new, v_new, slot_mapping, k_cache, v_cache, stream=None) -> N
     if v_cache.shape != k_cache.shape or slot_mapping.shape != (k_new.shape[0],):
         raise ValueError("cache or slot_mapping shape mismatch")
     dt = k_cache.dtype
-    guard, st = _on_device((k_new, v_new, slot_mapping, k_cache, v_cache), stream)
-    with guard:
-        _check(_lib.pa_kv_append(
-            _dev_ptr(k_new, "k_new", dt), _dev_ptr(v_new, "v_new", dt),
-            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
-            _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", dt), nb, bs, hkv, d,
-            _dtype_code(k_cache), st))
+    _call(_lib.pa_kv_append, (
+        _dev_ptr(k_new, "k_new", dt), _dev_ptr(v_new, "v_new", dt),
+        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", dt), nb, bs, hkv, d,
+        _dtype_code(k_cache)), (k_new, v_new, slot_mapping, k_cache, v_cache), stream)
 
 
 def pa_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
@@ -289,15 +313,13 @@ def pa_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_sc
         raise TypeError("caches must hold E4M3 codes (uint8 or float8_e4m3fn)")
     if k_scale.shape != (hkv,) or v_scale.shape != (hkv,):
         raise ValueError("k_scale/v_scale must be [num_kv_heads]")
-    guard, st = _on_device((k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale),
-                           stream)
-    with guard:
-        _check(_lib.pa_kv_append_fp8(
-            _dev_ptr(k_new, "k_new", torch.bfloat16), _dev_ptr(v_new, "v_new", torch.bfloat16),
-            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
-            _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-            _dev_ptr(k_scale, "k_scale", torch.float32),
-            _dev_ptr(v_scale, "v_scale", torch.float32), nb, bs, hkv, d, st))
+    _call(_lib.pa_kv_append_fp8, (
+        _dev_ptr(k_new, "k_new", torch.bfloat16), _dev_ptr(v_new, "v_new", torch.bfloat16),
+        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+        _dev_ptr(k_scale, "k_scale", torch.float32),
+        _dev_ptr(v_scale, "v_scale", torch.float32), nb, bs, hkv, d),
+        (k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale), stream)
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:
@@ -745,21 +767,21 @@ def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_c
         raise ValueError("k_scale and v_scale go with (and only with) E4M3 caches")
     if fp8 and (k_scale.shape != (hkv,) or v_scale.shape != (hkv,)):
         raise ValueError("k_scale/v_scale must be [num_kv_heads]")
-    opt = lambda t, nm, ty: None if t is None else _dev_ptr(t, nm, ty)  # noqa: E731
-    guard, st = _on_device((q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
-                            q_weight, k_weight, k_scale, v_scale), stream)
-    with guard:
-        (po, so), (pq, sq) = _dev_rows(q_out, "q_out", dt), _dev_rows(q, "q", dt)
-        (pk, sk), (pv, sv) = _dev_rows(k, "k", dt), _dev_rows(v, "v", dt)
-        _check(_lib.pa_qk_norm_rope_append(
-            po, pq, pk, pv, so, sq, sk, sv, _dev_ptr(positions, "positions", torch.int32),
-            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n,
-            _dev_ptr(cos_sin, "cos_sin", torch.float32), cos_sin.shape[0], cos_sin.shape[1],
-            int(bool(interleaved)), opt(q_weight, "q_weight", dt), opt(k_weight, "k_weight", dt),
-            float(eps), _dev_ptr(k_cache, "k_cache"),
-            _dev_ptr(v_cache, "v_cache", None if fp8 and _is_fp8(v_cache) else k_cache.dtype),
-            opt(k_scale, "k_scale", torch.float32), opt(v_scale, "v_scale", torch.float32), nb, bs,
-            hq, hkv, d, _dtype_code(k_cache), st))
+    (po, so), (pq, sq) = _dev_rows(q_out, "q_out", dt), _dev_rows(q, "q", dt)
+    (pk, sk), (pv, sv) = _dev_rows(k, "k", dt), _dev_rows(v, "v", dt)
+    f32 = torch.float32
+    _call(_lib.pa_qk_norm_rope_append, (
+        po, pq, pk, pv, so, sq, sk, sv, _dev_ptr(positions, "positions", torch.int32),
+        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n, _dev_ptr(cos_sin, "cos_sin", f32),
+        *cos_sin.shape, 1 if interleaved else 0,
+        None if q_weight is None else _dev_ptr(q_weight, "q_weight", dt),
+        None if k_weight is None else _dev_ptr(k_weight, "k_weight", dt), float(eps),
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", k_cache.dtype),
+        None if k_scale is None else _dev_ptr(k_scale, "k_scale", f32),
+        None if v_scale is None else _dev_ptr(v_scale, "v_scale", f32), nb, bs, hq, hkv, d,
+        _dtype_code(k_cache)),
+        (q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin, q_weight, k_weight,
+         k_scale, v_scale), stream)
 
 
 def pa_decode_tree_workspace_bytes(num_heads, num_kv_heads, head_dim, max_query_len) -> int:
@@ -789,19 +811,16 @@ def pa_decode_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_s
         raise ValueError("parents must be [total_q]")
     if workspace is None:
         raise ValueError("pa_decode_tree needs a workspace")
-    dt = k_cache.dtype
-    guard, st = _on_device((out, q, k_cache, v_cache, block_tables, context_lens, query_start,
-                            parents, workspace), stream)
-    with guard:
-        _check(_lib.pa_decode_tree(
-            _dev_ptr(out, "out", dt), _dev_ptr(q, "q", dt), _dev_ptr(k_cache, "k_cache"),
-            _dev_ptr(v_cache, "v_cache", dt), _dev_ptr(block_tables, "block_tables", torch.int32),
-            _dev_ptr(context_lens, "context_lens", torch.int32),
-            _dev_ptr(query_start, "query_start", torch.int32),
-            None if parents is None else _dev_ptr(parents, "parents", torch.int32), s, total_q, hq,
-            hkv, d, bs, nb, block_tables.shape[1], int(max_query_len), float(scale),
-            _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-            _dtype_code(k_cache), st))
+    dt, i32 = k_cache.dtype, torch.int32
+    _call(_lib.pa_decode_tree, (
+        _dev_ptr(out, "out", dt), _dev_ptr(q, "q", dt), _dev_ptr(k_cache, "k_cache"),
+        _dev_ptr(v_cache, "v_cache", dt), _dev_ptr(block_tables, "block_tables", i32),
+        _dev_ptr(context_lens, "context_lens", i32), _dev_ptr(query_start, "query_start", i32),
+        None if parents is None else _dev_ptr(parents, "parents", i32), s, total_q, hq, hkv, d, bs,
+        nb, block_tables.shape[1], int(max_query_len), float(scale), _dev_ptr(workspace, "workspace"),
+        workspace.nbytes, _dtype_code(k_cache)),
+        (out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents, workspace),
+        stream)
 
 
 def _prob_rows(t, name, rows, vocab):
@@ -839,19 +858,18 @@ def pa_verify_draft(out_tokens, out_path, out_len, target_probs, draft_probs, dr
         if t is not None and t.shape != (total_q,):
             raise ValueError(f"{name} must be [total_q]")
     i32, f32 = torch.int32, torch.float32
-    guard, st = _on_device((out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens,
-                            parents, query_start, u_accept, u_sample), stream)
-    with guard:
-        pt, ts = _prob_rows(target_probs, "target_probs", total_q, vocab)
-        pd, ds = (None, 0) if draft_probs is None else \
-            _prob_rows(draft_probs, "draft_probs", total_q, vocab)
-        _check(_lib.pa_verify_draft(
-            _dev_ptr(out_tokens, "out_tokens", i32), _dev_ptr(out_path, "out_path", i32),
-            _dev_ptr(out_len, "out_len", i32), pt, ts, pd, ds,
-            _dev_ptr(draft_tokens, "draft_tokens", i32),
-            None if parents is None else _dev_ptr(parents, "parents", i32),
-            _dev_ptr(query_start, "query_start", i32), _dev_ptr(u_accept, "u_accept", f32),
-            _dev_ptr(u_sample, "u_sample", f32), s, total_q, vocab, most, st))
+    pt, ts = _prob_rows(target_probs, "target_probs", total_q, vocab)
+    pd, ds = (None, 0) if draft_probs is None else \
+        _prob_rows(draft_probs, "draft_probs", total_q, vocab)
+    _call(_lib.pa_verify_draft, (
+        _dev_ptr(out_tokens, "out_tokens", i32), _dev_ptr(out_path, "out_path", i32),
+        _dev_ptr(out_len, "out_len", i32), pt, ts, pd, ds,
+        _dev_ptr(draft_tokens, "draft_tokens", i32),
+        None if parents is None else _dev_ptr(parents, "parents", i32),
+        _dev_ptr(query_start, "query_start", i32), _dev_ptr(u_accept, "u_accept", f32),
+        _dev_ptr(u_sample, "u_sample", f32), s, total_q, vocab, most),
+        (out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens, parents,
+         query_start, u_accept, u_sample), stream)
 
 
 def pa_kv_accept(k_cache, v_cache, block_tables, context_lens, query_start, path, path_len,
@@ -872,15 +890,13 @@ def pa_kv_accept(k_cache, v_cache, block_tables, context_lens, query_start, path
     if path.dim() != 2 or path.shape[0] != s or path_len.shape != (s,):
         raise ValueError("path must be [S, max_path_len], path_len [S]")
     i32 = torch.int32
-    guard, st = _on_device((k_cache, v_cache, block_tables, context_lens, query_start, path,
-                            path_len), stream)
-    with guard:
-        _check(_lib.pa_kv_accept(
-            _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", k_cache.dtype),
-            _dev_ptr(block_tables, "block_tables", i32), _dev_ptr(context_lens, "context_lens", i32),
-            _dev_ptr(query_start, "query_start", i32), _dev_ptr(path, "path", i32),
-            _dev_ptr(path_len, "path_len", i32), s, path.shape[1], nb, bs, block_tables.shape[1],
-            hkv, d, _dtype_code(k_cache), st))
+    _call(_lib.pa_kv_accept, (
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", k_cache.dtype),
+        _dev_ptr(block_tables, "block_tables", i32), _dev_ptr(context_lens, "context_lens", i32),
+        _dev_ptr(query_start, "query_start", i32), _dev_ptr(path, "path", i32),
+        _dev_ptr(path_len, "path_len", i32), s, path.shape[1], nb, bs, block_tables.shape[1], hkv,
+        d, _dtype_code(k_cache)),
+        (k_cache, v_cache, block_tables, context_lens, query_start, path, path_len), stream)
 
 
 def pa_device_errors(stream=None) -> int:

@@ -38,21 +38,27 @@ struct RowsParams {
   int64_t num_slots;
   int num_tokens, num_heads, num_kv_heads, max_position, rotary_dim;
   unsigned units_per_token;
+  int q_units, kv_units;  // of a token: of its q heads, of its k heads (and of its v heads)
   float eps;
 };
 
 // Rows of T; a lane holds 16 bytes of a head's row, kLanes lanes a row, so a
-// warp instruction moves kRows rows. A unit of work is U such instructions of
-// one token (its q heads, then k, then v heads); one warp per unit, all its
-// loads first (before the position is known). HBM-bound: every row is read and written once, the cosines and
-// sines of a token once per unit from L1/L2.
+// warp instruction moves kRows rows. A unit of work is U such instructions of q
+// heads, of k heads or of v heads of one token; one warp per unit, all its loads
+// first (before the position is known). The bytes bound it (every row is read
+// and written once), if the instructions stay few: with the weights folded into
+// the cosines and sines once per unit,
+//   out[e] = r (x[e] cw[e] + z[e] sw[e]),  r = 1 / sqrt(mean(x^2) + eps),
+// z[e] the other element of the pair (its lane's 16 bytes are shuffled, not its
+// floats), all two elements to an instruction.
 template <typename T, int D>
 struct RowsConfig {
   static constexpr int kEPL = ElemTraits<T>::kPer16B;
   static constexpr int kLanes = D / kEPL;
   static constexpr int kRows = 32 / kLanes;
   static constexpr int kU = 4;
-  static constexpr int kWarps = 4;  // per CTA
+  static constexpr int kPer = kRows * kU;  // heads of a unit
+  static constexpr int kWarps = 4;         // per CTA
 };
 
 // N consecutive floats (N = 2, 4, 8; N * 4 or 16 bytes aligned).
@@ -74,162 +80,183 @@ __device__ __forceinline__ void load_floats(const float* p, float (&x)[N]) {
   }
 }
 
+// 16 bytes of a row as pairs of floats.
+template <typename T, int N>
+__device__ __forceinline__ void unpack_pairs(const uint4& v, uint64_t (&x)[N]) {
+  float f[2 * N];
+  ElemTraits<T>::unpack(v, f);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = pair_of(f[2 * i], f[2 * i + 1]);
+}
+
 template <typename T, int D, bool FP8, bool INTERLEAVED>
 __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
     qk_norm_rope_append_kernel(const RowsParams p) {
   using Cfg = RowsConfig<T, D>;
-  constexpr int EPL = Cfg::kEPL, LPR = Cfg::kLanes, U = Cfg::kU;
+  constexpr int EPL = Cfg::kEPL, LPR = Cfg::kLanes, U = Cfg::kU, NP = EPL / 2;
   pdl_wait();
   pdl_launch_dependents();
   const unsigned unit = blockIdx.x * Cfg::kWarps + (threadIdx.x >> 5);
   const unsigned tok = unit / p.units_per_token;
   if (tok >= static_cast<unsigned>(p.num_tokens)) return;
-  const int lane = threadIdx.x & 31, li = lane % LPR;
+  const int part = static_cast<int>(unit - tok * p.units_per_token);
+  const int lane = threadIdx.x & 31, li = lane % LPR, e0 = li * EPL;
   const int pos = __ldg(p.positions + tok);
   const int64_t slot = __ldg(p.slots + tok);
-  const int row0 = static_cast<int>(unit - tok * p.units_per_token) * (U * Cfg::kRows) + lane / LPR;
-  const int hq = p.num_heads, hkv = p.num_kv_heads, total = hq + 2 * hkv;
-
-  // rows of this unit: kind 0 q, 1 k, 2 v, 3 none
-  int kind[U], head[U];
+  // kind 0 q, 1 k, 2 v (the same for the warp), and its heads
+  const int kind = part < p.q_units ? 0 : part < p.q_units + p.kv_units ? 1 : 2;
+  const int heads = kind == 0 ? p.num_heads : p.num_kv_heads;
+  const int head0 = (part - (kind == 0 ? 0 : kind == 1 ? p.q_units : p.q_units + p.kv_units)) * Cfg::kPer +
+                    lane / LPR;
+  const T* src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                 tok * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + head0 * D + e0;
   uint4 raw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int r = row0 + u * Cfg::kRows;
-    kind[u] = r < hq ? 0 : r < hq + hkv ? 1 : r < total ? 2 : 3;
-    head[u] = kind[u] == 0 ? r : kind[u] == 1 ? r - hq : r - hq - hkv;
     raw[u] = make_uint4(0, 0, 0, 0);
-    if (kind[u] != 3) {
-      const T* base = static_cast<const T*>(kind[u] == 0 ? p.q : kind[u] == 1 ? p.k : p.v);
-      const int64_t st = kind[u] == 0 ? p.q_stride : kind[u] == 1 ? p.k_stride : p.v_stride;
-      // (not the read-only path: q_out may be q)
-      raw[u] = __ldcs(reinterpret_cast<const uint4*>(base + tok * st + head[u] * D + li * EPL));
-    }
+    // (not the read-only path: q_out may be q)
+    if (head0 + u * Cfg::kRows < heads)
+      raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * Cfg::kRows * D));
   }
   if (pos < 0) return;  // padding
-  if (pos >= p.max_position || slot >= p.num_slots) {
-    if (lane == 0 && row0 == 0)
-      atomicOr(p.err, pos >= p.max_position ? PA_DEVERR_POSITION : PA_DEVERR_SLOT);
-    if (pos >= p.max_position) return;
+  if (pos >= p.max_position) {
+    if (lane == 0 && part == 0) atomicOr(p.err, PA_DEVERR_POSITION);
+    return;
   }
-  if (slot < 0 || slot >= p.num_slots) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (kind[u] != 0) kind[u] = 3;
-  }
-  // cosines and sines of this lane's elements
+  if (slot >= p.num_slots && lane == 0 && part == 0) atomicOr(p.err, PA_DEVERR_SLOT);
+  if (kind != 0 && (slot < 0 || slot >= p.num_slots)) return;
+  uint8_t* cache = static_cast<uint8_t*>(kind == 1 ? p.k_cache : p.v_cache);
+  const int64_t cache_row = slot * p.num_kv_heads + head0;
+  T* dst = kind == 0 ? static_cast<T*>(p.q_out) + tok * p.q_out_stride + head0 * D + e0
+                     : reinterpret_cast<T*>(cache) + cache_row * D + e0;
+
+  uint64_t cw[NP], sw[NP];
+  int partner = lane;  // lane that holds the other elements of this lane's pairs
   const int half = p.rotary_dim >> 1;
-  const int e0 = li * EPL;
   const bool rotated = e0 < p.rotary_dim;
-  constexpr int NC = INTERLEAVED ? EPL / 2 : EPL;
-  float cs[NC], sn[NC];
-  int partner = lane;  // lane that holds the other halves of this lane's pairs
-  if (rotated) {
-    const float* c = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim +
-                     (INTERLEAVED ? e0 / 2 : e0 < half ? e0 : e0 - half);
-    load_floats<NC>(c, cs);
-    load_floats<NC>(c + half, sn);
-    if (!INTERLEAVED) {
-      partner = e0 < half ? lane + half / EPL : lane - half / EPL;
-      if (e0 < half) {
+  const T* weight = static_cast<const T*>(kind == 0 ? p.q_weight : p.k_weight);
+  if (kind < 2) {
+    float c[EPL], n[EPL], w[EPL], wp[EPL];
+    if (rotated) {
+      constexpr int NC = INTERLEAVED ? NP : EPL;
+      float cs[NC], sn[NC];
+      const float* t = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim +
+                       (INTERLEAVED ? e0 / 2 : e0 < half ? e0 : e0 - half);
+      load_floats<NC>(t, cs);
+      load_floats<NC>(t + half, sn);
+      if (!INTERLEAVED) partner = e0 < half ? lane + half / EPL : lane - half / EPL;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) sn[i] = -sn[i];
+      for (int e = 0; e < EPL; ++e) {
+        c[e] = cs[INTERLEAVED ? e / 2 : e];
+        const bool first = INTERLEAVED ? e % 2 == 0 : e0 < half;
+        n[e] = first ? -sn[INTERLEAVED ? e / 2 : e] : sn[INTERLEAVED ? e / 2 : e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        c[e] = 1.0f;
+        n[e] = 0.0f;
       }
     }
+    if (weight != nullptr) {
+      ElemTraits<T>::unpack(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
+      if (INTERLEAVED) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) wp[e] = w[e ^ 1];
+      } else {
+        ElemTraits<T>::unpack(__ldg(reinterpret_cast<const uint4*>(weight + (partner % LPR) * EPL)), wp);
+      }
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        c[e] *= w[e];
+        n[e] *= wp[e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      cw[i] = pair_of(c[2 * i], c[2 * i + 1]);
+      sw[i] = pair_of(n[2 * i], n[2 * i + 1]);
+    }
   }
-  const int pe0 = (partner % LPR) * EPL;
 
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    float x[EPL];
-    ElemTraits<T>::unpack(raw[u], x);
-    if (__any_sync(kFullMask, kind[u] < 2)) {  // (a v row is copied as it is)
-      float rs = 1.0f, w[EPL], wp[EPL];
-      const T* weight = static_cast<const T*>(kind[u] == 0 ? p.q_weight : p.k_weight);
-      if (__any_sync(kFullMask, weight != nullptr && kind[u] < 2)) {
-        float ss = 0.0f;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
-        if (weight != nullptr) rs = rsqrtf(ss * (1.0f / D) + p.eps);
-      }
-      if (weight != nullptr) {
-        ElemTraits<T>::unpack(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
-        if (!INTERLEAVED) ElemTraits<T>::unpack(__ldg(reinterpret_cast<const uint4*>(weight + pe0)), wp);
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) w[e] = wp[e] = 1.0f;
-      }
-      float y[EPL];
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) y[e] = x[e] * rs * w[e];
+    if (u > 0 && head0 - lane / LPR + u * Cfg::kRows >= heads) break;  // (the same for the warp)
+    const bool on = head0 + u * Cfg::kRows < heads;
+    uint64_t y[NP];
+    if (kind < 2) {
+      uint64_t x[NP], z[NP];
+      unpack_pairs<T>(raw[u], x);
       if constexpr (INTERLEAVED) {
-        if (rotated) {
 #pragma unroll
-          for (int i = 0; i < EPL / 2; ++i) {
-            const float a = y[2 * i], b = y[2 * i + 1];
-            y[2 * i] = a * cs[i] - b * sn[i];
-            y[2 * i + 1] = b * cs[i] + a * sn[i];
-          }
+        for (int i = 0; i < NP; ++i) {
+          float lo, hi;
+          floats_of(x[i], lo, hi);
+          z[i] = rotated ? pair_of(hi, lo) : 0;
         }
       } else {
-        // the partner's raw 16 bytes (fewer shuffles than its normed floats)
         uint4 o;
         o.x = __shfl_sync(kFullMask, raw[u].x, partner);
         o.y = __shfl_sync(kFullMask, raw[u].y, partner);
         o.z = __shfl_sync(kFullMask, raw[u].z, partner);
         o.w = __shfl_sync(kFullMask, raw[u].w, partner);
-        float z[EPL];
-        ElemTraits<T>::unpack(o, z);
-        if (rotated) {
-#pragma unroll
-          for (int e = 0; e < EPL; ++e) y[e] = y[e] * cs[e] + z[e] * rs * wp[e] * sn[e];
-        }
+        if (!rotated) o = make_uint4(0, 0, 0, 0);  // (an infinite x is not a pair of itself)
+        unpack_pairs<T>(o, z);
       }
-      if (kind[u] < 2) {
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) x[e] = y[e];
-      }
-    }
-    if (kind[u] == 3) continue;
-    if (FP8 && kind[u] != 0) {
-      // one rounding: the float32 row divided by its head's scale, to E4M3
-      const float sc = __ldg((kind[u] == 1 ? p.k_scale : p.v_scale) + head[u]);
-      uint32_t r[EPL / 4];
+      for (int i = 0; i < NP; ++i) y[i] = fma2(z[i], sw[i], mul2(x[i], cw[i]));
+      if (weight != nullptr) {
+        uint64_t sq = mul2(x[0], x[0]);
 #pragma unroll
-      for (int i = 0; i < EPL / 4; ++i)
-        r[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(x[4 * i], sc), __fdiv_rn(x[4 * i + 1], sc))) |
-               (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(x[4 * i + 2], sc), __fdiv_rn(x[4 * i + 3], sc))) << 16);
-      uint8_t* dst = static_cast<uint8_t*>(kind[u] == 1 ? p.k_cache : p.v_cache) +
-                     (slot * hkv + head[u]) * D + e0;
-      if constexpr (EPL == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(r[0], r[1]);
-      continue;
-    }
-    uint4 o;
-    if constexpr (EPL == 8) {
-      // v: its own bits; q and k: one rounding from float32
-      if (kind[u] == 2) {
-        o = raw[u];
-      } else {
-        o = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4 % EPL], x[5 % EPL]),
-                       pack_bf16x2(x[6 % EPL], x[7 % EPL]));
+        for (int i = 1; i < NP; ++i) sq = fma2(x[i], x[i], sq);
+        float s0, s1;
+        floats_of(sq, s0, s1);
+        float ss = s0 + s1;
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kFullMask, ss, o);
+        const float r = rsqrtf(ss * (1.0f / D) + p.eps);
+        const uint64_t rr = pair_of(r, r);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) y[i] = mul2(y[i], rr);
       }
     } else {
-      o = make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+      unpack_pairs<T>(raw[u], y);
     }
-    T* dst = kind[u] == 0 ? static_cast<T*>(p.q_out) + tok * p.q_out_stride + head[u] * D + e0
-                          : static_cast<T*>(kind[u] == 1 ? p.k_cache : p.v_cache) +
-                                (slot * hkv + head[u]) * D + e0;
-    *reinterpret_cast<uint4*>(dst) = o;
+    if (!on) continue;
+    float f[EPL];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) floats_of(y[i], f[2 * i], f[2 * i + 1]);
+    if (FP8 && kind != 0) {
+      // one rounding: the float32 row divided by its head's scale, to E4M3
+      if constexpr (EPL == 8) {
+        const float sc = __ldg((kind == 1 ? p.k_scale : p.v_scale) + head0 + u * Cfg::kRows);
+        uint32_t r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          r[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(f[4 * i], sc), __fdiv_rn(f[4 * i + 1], sc))) |
+                 (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(f[4 * i + 2], sc), __fdiv_rn(f[4 * i + 3], sc))) << 16);
+        *reinterpret_cast<uint2*>(cache + (cache_row + u * Cfg::kRows) * D + e0) = make_uint2(r[0], r[1]);
+      }
+      continue;
+    }
+    uint4 o = raw[u];  // v: its own bits
+    if (kind != 2) {
+      if constexpr (EPL == 8)
+        o = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                       pack_bf16x2(f[6], f[7]));
+      else
+        o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+    *reinterpret_cast<uint4*>(dst + u * Cfg::kRows * D) = o;
   }
 }
 
 template <typename T, int D, bool FP8>
 cudaError_t launch_rows_t(RowsParams p, bool interleaved, cudaStream_t stream) {
   using Cfg = RowsConfig<T, D>;
-  const int rows = p.num_heads + 2 * p.num_kv_heads, per = Cfg::kRows * Cfg::kU;
-  p.units_per_token = static_cast<unsigned>((rows + per - 1) / per);
+  p.q_units = (p.num_heads + Cfg::kPer - 1) / Cfg::kPer;
+  p.kv_units = (p.num_kv_heads + Cfg::kPer - 1) / Cfg::kPer;
+  p.units_per_token = static_cast<unsigned>(p.q_units + 2 * p.kv_units);
   const int64_t units = static_cast<int64_t>(p.num_tokens) * p.units_per_token;
   if (units > 0x7fffffff) return cudaErrorNotSupported;
   const dim3 grid(static_cast<unsigned>((units + Cfg::kWarps - 1) / Cfg::kWarps));
@@ -406,28 +433,30 @@ struct VerifyParams {
   int total_rows, vocab, max_query_len;
 };
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
-constexpr int kVerifyBatch = 4;  // groups of 128 values that a warp loads at once
+constexpr int kVerifyBatch = 4;  // groups of 128 values that a warp takes at once
+constexpr int kVerifyChunk = 128 * kVerifyBatch;
+constexpr int kVerifyStages = 3;  // of a warp's ring: a chunk of p and one of q each
+constexpr int kVerifyRing = kVerifyWarps * kVerifyStages * kVerifyChunk * 8;
 
-// The mass left of a target row after the rejections at one node,
-//   sampled drafts: R_0 = p, R_{k+1} = max(R_k / Z_k - q, 0), Z_k = sum R_k (Z_0 = 1).
-// Where R_k > 0 it is A_k p - B_k q with A_{k+1} = A_k / Z_k, B_{k+1} = B_k / Z_k + 1,
-// and where it is 0, A_{k+1} p - B_{k+1} q <= -q <= 0: so R_k = max(A_k p - B_k q, 0)
-// for every k, and two numbers stand for any number of rejections.
+// The mass left of a target row p after rejections at one node,
+//   sampled drafts: R_0 = p, Z_0 = 1, R_{k+1} = max(R_k / Z_k - q, 0), Z_k = sum R_k.
+// Where R_k > 0 it is A_k (p - t_k q), and where it is 0 the next one is 0 too; with
+// F(t) = sum max(p - t q, 0), Z_k = A_k F(t_k), A_{k+1} = 1 / F(t_k) and
+// t_{k+1} = t_k + F(t_k) (t_0 = 0, F counted as 1 there). A cancels from every
+// comparison: one number t stands for any number of rejections, child x is
+// accepted where u q(x) F(t) < max(p(x) - t q(x), 0), and the last token is drawn
+// from max(p - t q, 0).
 //   picked drafts (q one-hot): R = p without the rejected tokens.
-// Values that are not > 0 count as 0.
 struct Residual {
-  double a, b;       // sampled drafts
-  int gone;          // picked drafts: rejected tokens so far (their list is in shared memory)
+  double t;  // sampled drafts
+  int gone;  // picked drafts: rejected tokens so far (their list is in shared memory)
 };
 
-__device__ __forceinline__ double mass_of(float p, float q, double a, double b) {
-  const double x = p > 0.0f ? static_cast<double>(p) : 0.0;
-  if (b == 0.0) return x;
-  const double y = q > 0.0f ? static_cast<double>(q) : 0.0;
-  const double r = a * x - b * y;
-  return r > 0.0 ? r : 0.0;
+__device__ __forceinline__ double mass_of(float p, float q, double t) {
+  const double r = static_cast<double>(p) - t * (q > 0.0f ? static_cast<double>(q) : 0.0);
+  return r > 0.0 ? r : 0.0;  // (NaN: 0)
 }
 
 // One cluster of CTAs per sequence. Every CTA walks the rows in order with the
@@ -436,26 +465,32 @@ __device__ __forceinline__ double mass_of(float p, float q, double a, double b) 
 // token read up front by one thread. Sums over the vocabulary are split over
 // the cluster's warps, a contiguous piece each, in 64 bits: a sampled draft's
 // mass only when a later child is tried, and the last token's at the end, whose
-// piece is then searched by one warp. Bound by reading one row of p and one of
-// q per sequence.
+// piece is then searched. All in float64. Bound by reading one row of p and one of
+// q per sequence, and by their passes from L2 for further children.
 template <bool VEC>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  // per row: p(token), q(token), u, token, parent; then the rejected tokens' list
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  // the warps' rings; per row p(token), q(token), u, token, parent; then the
+  // rejected tokens' list
   const int cap = p.max_query_len;
-  float* s_p = reinterpret_cast<float*>(smem_raw);
+  float* s_p = reinterpret_cast<float*>(smem_raw + (VEC ? kVerifyRing : 0));
   float* s_q = s_p + cap;
   float* s_u = s_q + cap;
   int* s_tok = reinterpret_cast<int*>(s_u + cap);
   int* s_par = s_tok + cap;
   int* s_gone = s_par + cap;
   __shared__ double s_warp[kVerifyWarps], s_rank[2][8];
+  __shared__ uint64_t s_bar[kVerifyWarps][kVerifyStages];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / ranks;
 
+  if (VEC && lane == 0) {
+    for (int i = 0; i < kVerifyStages; ++i) mbar_init(smem_u32(&s_bar[warp][i]), 1);
+    fence_barrier_init();
+  }
   pdl_wait();
   pdl_launch_dependents();
   const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
@@ -508,10 +543,10 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       for (int e = 0; e < 4; ++e) x[e] = i + e < p.vocab ? __ldg(row + i + e) : 0.0f;
     }
   };
-  // the residual's masses of kVerifyBatch groups of 4 values of row `cur`: lane's
-  // own of the 128 from i0 on, of the next 128, ... (0 from hi on); all loads first
-  auto masses = [&](int cur, const Residual& r, int i0, double (&m)[kVerifyBatch][4]) {
-    float x[kVerifyBatch][4], y[kVerifyBatch][4];
+  // p and q of kVerifyBatch groups of 4 values of row `cur`: lane's own of the 128
+  // from i0 on, of the next 128, ... (0 from `end` on); all loads first
+  auto load_batch = [&](int cur, const Residual& r, int i0, int end, float (&x)[kVerifyBatch][4],
+                        float (&y)[kVerifyBatch][4]) {
     const float* prow = p.target + (q0 + cur) * p.target_stride;
     const float* qrow = p.draft + (q0 + cur) * p.draft_stride;
 #pragma unroll
@@ -519,37 +554,106 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       const int i = i0 + u * 128 + lane * 4;
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[u][e] = y[u][e] = 0.0f;
-      if (i < hi) {
+      if (i < end) {
         load4(prow, i, x[u]);
-        if (r.b != 0.0) load4(qrow, i, y[u]);
+        if (r.t != 0.0) load4(qrow, i, y[u]);
       }
     }
+  };
+  // the masses of values i .. i + 3, from their p and q
+  auto masses = [&](const Residual& r, int i, const float (&x)[4], const float (&y)[4], double (&m)[4]) {
+    if (r.t != 0.0) {
 #pragma unroll
-    for (int u = 0; u < kVerifyBatch; ++u) {
-      const int i = i0 + u * 128 + lane * 4;
+      for (int e = 0; e < 4; ++e) {
+        const double d = fma(-r.t, static_cast<double>(fmaxf(y[e], 0.0f)), static_cast<double>(fmaxf(x[e], 0.0f)));
+        const int keep = ~(__double2hiint(d) >> 31);  // by its sign (no NaN can be here)
+        m[e] = __hiloint2double(__double2hiint(d) & keep, __double2loint(d) & keep);
+      }
+    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m[u][e] = mass_of(x[u][e], y[u][e], r.a, r.b);
+      for (int e = 0; e < 4; ++e) m[e] = static_cast<double>(fmaxf(x[e], 0.0f));
       for (int g = 0; g < r.gone; ++g) {
         const int t = s_gone[g] - i;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (t == e) m[u][e] = 0.0;
+          if (t == e) m[e] = 0.0;
       }
     }
+  };
+  // This warp's ring: chunks arrive by bulk copies while earlier ones are summed (a
+  // warp's own loads would hold too few bytes in flight: a pass of 128,256 values
+  // took 24 us in one CTA of 512 threads). A chunk's use of the ring goes on from
+  // the last one's, over all sums.
+  const uint32_t ring = smem_u32(smem_raw) + warp * kVerifyStages * kVerifyChunk * 8;
+  int ring_st = 0;
+  uint32_t ring_ph = 0;
+  auto fetch = [&](int cur, const Residual& r, int i0, int end, int st) {
+    if (lane != 0) return;
+    const uint32_t bytes = static_cast<uint32_t>(min(kVerifyChunk, end - i0) & ~3) * 4;
+    const uint32_t bar = smem_u32(&s_bar[warp][st]), dst = ring + st * kVerifyChunk * 8;
+    const bool both = r.t != 0.0;
+    mbar_arrive_expect_tx(bar, both ? 2 * bytes : bytes);
+    if (bytes == 0) return;
+    bulk_load(dst, p.target + (q0 + cur) * p.target_stride + i0, bytes, bar);
+    if (both) bulk_load(dst + kVerifyChunk * 4, p.draft + (q0 + cur) * p.draft_stride + i0, bytes, bar);
+  };
+  // a warp's sum over values [a, b)
+  auto sum_of = [&](int cur, const Residual& r, int a, int b) {
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    if (VEC) {
+#pragma unroll
+      for (int k = 0; k < kVerifyStages; ++k)
+        if (a + k * kVerifyChunk < b) fetch(cur, r, a + k * kVerifyChunk, b, (ring_st + k) % kVerifyStages);
+    }
+    for (int i0 = a; i0 < b; i0 += kVerifyChunk) {
+      float x[kVerifyBatch][4], y[kVerifyBatch][4];
+      if constexpr (VEC) {
+        mbar_wait(smem_u32(&s_bar[warp][ring_st]), ring_ph, p.err);
+        const uint32_t src = ring + ring_st * kVerifyChunk * 8 + lane * 16;
+#pragma unroll
+        for (int u = 0; u < kVerifyBatch; ++u) {
+          const int i = i0 + u * 128 + lane * 4;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[u][e] = y[u][e] = 0.0f;
+          if (i + 4 <= b) {
+            const uint4 px = lds128(src + u * 512);
+            ElemTraits<float>::unpack(px, x[u]);
+            if (r.t != 0.0) ElemTraits<float>::unpack(lds128(src + kVerifyChunk * 4 + u * 512), y[u]);
+          } else if (i < b) {  // the vocabulary's last one to three values
+            load4(p.target + (q0 + cur) * p.target_stride, i, x[u]);
+            if (r.t != 0.0) load4(p.draft + (q0 + cur) * p.draft_stride, i, y[u]);
+          }
+        }
+      } else {
+        load_batch(cur, r, i0, b, x, y);
+      }
+#pragma unroll
+      for (int u = 0; u < kVerifyBatch; ++u) {
+        double m[4];
+        masses(r, i0 + u * 128 + lane * 4, x[u], y[u], m);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] += m[e];
+      }
+      if constexpr (VEC) {
+        __syncwarp();  // every lane has read the chunk
+        if (i0 + kVerifyStages * kVerifyChunk < b)
+          fetch(cur, r, i0 + kVerifyStages * kVerifyChunk, b, ring_st);
+        if (++ring_st == kVerifyStages) {
+          ring_st = 0;
+          ring_ph ^= 1;
+        }
+      }
+    }
+    double t = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFullMask, t, o);
+    return t;
   };
   int turn = 0;
   // the sum over the vocabulary; s_warp then holds the pieces' sums of this
   // CTA and s_rank[which] the CTAs'
   auto total_mass = [&](int cur, const Residual& r, int* which) {
-    double acc = 0.0;
-    for (int i0 = lo; i0 < hi; i0 += 128 * kVerifyBatch) {
-      double m[kVerifyBatch][4];
-      masses(cur, r, i0, m);
-#pragma unroll
-      for (int u = 0; u < kVerifyBatch; ++u) acc += (m[u][0] + m[u][1]) + (m[u][2] + m[u][3]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(kFullMask, acc, o);
+    const double acc = sum_of(cur, r, lo, hi);
     __syncthreads();  // (earlier readers of s_warp are done)
     if (lane == 0) s_warp[warp] = acc;
     __syncthreads();
@@ -567,7 +671,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
   };
 
   int cur = 0, len = 1, which = 0;
-  Residual r{1.0, 0.0, 0};
+  Residual r{0.0, 0};
   double z = 1.0;
   bool stale = false;  // z has not been summed since the last rejection
   if (rank == 0 && tid == 0) out_path[0] = 0;
@@ -577,7 +681,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       z = total_mass(cur, r, &which);
       stale = false;
     }
-    double left = mass_of(s_p[i], s_q[i], r.a, r.b);
+    double left = mass_of(s_p[i], s_q[i], r.t);
     for (int g = 0; g < r.gone; ++g)
       if (s_gone[g] == s_tok[i]) left = 0.0;
     const double qx = s_q[i] > 0.0f ? static_cast<double>(s_q[i]) : 0.0;
@@ -588,13 +692,12 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       }
       cur = i;
       ++len;
-      r = Residual{1.0, 0.0, 0};
+      r = Residual{0.0, 0};
       z = 1.0;
       continue;
     }
     if (p.draft != nullptr) {
-      // (nothing left: stays so)
-      r = z > 0.0 ? Residual{r.a / z, r.b / z + 1.0, 0} : Residual{0.0, 1.0, 0};
+      r.t += z;
       stale = true;
     } else {
       z = fmax(z - left, 0.0);
@@ -606,7 +709,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
   }
   z = total_mass(cur, r, &which);
   if (!(z > 0.0)) {  // nothing left: the target's own row
-    r = Residual{1.0, 0.0, 0};
+    r = Residual{0.0, 0};
     z = total_mass(cur, r, &which);
   }
   // the lowest index whose running sum exceeds u z: its CTA, its warp's piece, its place
@@ -634,34 +737,52 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       at_before = last_before;
     }
     if (good && rank == at) {
-      double b2 = at_before, w_before = 0.0, wl_before = 0.0;
-      int aw = -1, lw = -1;
-      for (int w = 0; w < kVerifyWarps; ++w) {
-        const double t = s_warp[w];
-        if (t > 0.0) {
-          lw = w;
-          wl_before = b2;
+      // the first place of n whose running sum passes `want` (else the last with
+      // a sum), and the sum before it
+      auto place = [&](const double* sums, int n, double& run) {
+        double b2 = run, first_before = 0.0, last_before = 0.0;
+        int first = -1, end = -1;
+        for (int w = 0; w < n; ++w) {
+          const double t = sums[w];
+          if (t > 0.0) {
+            end = w;
+            last_before = b2;
+          }
+          if (first < 0 && b2 + t > want) {
+            first = w;
+            first_before = b2;
+          }
+          b2 += t;
         }
-        if (aw < 0 && b2 + t > want) {
-          aw = w;
-          w_before = b2;
-        }
-        b2 += t;
+        run = first >= 0 ? first_before : last_before;
+        return first >= 0 ? first : end;
+      };
+      double run = at_before;
+      int w = place(s_warp, kVerifyWarps, run);
+      int a = min((rank * kVerifyWarps + w) * per * 128, p.vocab);
+      int b = min(a + per * 128, p.vocab);
+      if (per > kVerifyBatch) {
+        // a long piece: the CTA's warps sum a part each, and one of them has it
+        const int step = (per + kVerifyWarps - 1) / kVerifyWarps * 128;
+        const int sub = min(a + warp * step, b);
+        const double t = sum_of(cur, r, sub, min(sub + step, b));
+        __syncthreads();
+        if (lane == 0) s_warp[warp] = t;
+        __syncthreads();
+        w = place(s_warp, kVerifyWarps, run);
+        a = min(a + w * step, b);
+        b = min(a + step, b);
       }
-      if (aw < 0) {
-        aw = lw;
-        w_before = wl_before;
-      }
-      if (warp == aw) {
-        double run = w_before;
+      if (warp == w) {
         int last_pos = -1;
-        for (int i0 = lo; i0 < hi && chosen < 0; i0 += 128 * kVerifyBatch) {
-          double mm[kVerifyBatch][4];
-          masses(cur, r, i0, mm);
+        for (int i0 = a; i0 < b && chosen < 0; i0 += kVerifyChunk) {
+          float x[kVerifyBatch][4], y[kVerifyBatch][4];
+          load_batch(cur, r, i0, b, x, y);
 #pragma unroll
           for (int u = 0; u < kVerifyBatch; ++u) {
             const int i = i0 + u * 128 + lane * 4;
-            const double(&m)[4] = mm[u];
+            double m[4];
+            masses(r, i, x[u], y[u], m);
             const double c0 = m[0], c1 = c0 + m[1], c2 = c1 + m[2], c3 = c2 + m[3];
             double incl = c3;
 #pragma unroll
@@ -669,9 +790,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
               const double t = __shfl_up_sync(kFullMask, incl, o);
               if (lane >= o) incl += t;
             }
-            const double b = run + (incl - c3);
-            const int hit = m[0] > 0.0 && b + c0 > want ? 0 : m[1] > 0.0 && b + c1 > want ? 1
-                            : m[2] > 0.0 && b + c2 > want ? 2 : m[3] > 0.0 && b + c3 > want ? 3 : 4;
+            const double bb = run + (incl - c3);
+            const int hit = m[0] > 0.0 && bb + c0 > want ? 0 : m[1] > 0.0 && bb + c1 > want ? 1
+                            : m[2] > 0.0 && bb + c2 > want ? 2 : m[3] > 0.0 && bb + c3 > want ? 3 : 4;
             const int lastp = m[3] > 0.0 ? 3 : m[2] > 0.0 ? 2 : m[1] > 0.0 ? 1 : m[0] > 0.0 ? 0 : -1;
             const unsigned hits = __ballot_sync(kFullMask, hit < 4);
             const unsigned pos = __ballot_sync(kFullMask, lastp >= 0);
@@ -723,6 +844,8 @@ cudaError_t launch_verify_draft(const VerifyShape& sh, int32_t* out_tokens, int3
   if (e != cudaSuccess) return e;
   // CTAs per sequence: as many (up to the portable 8) as keep the launch within
   // one wave of resident CTAs (two an SM) and leave each a few thousand values
+  // (128,256 values, one draw a sequence: 64 sequences 13.3 us with 4 CTAs, 20.4
+  // with 8; 256 sequences 36 with 1, 52 with 4; one sequence 9.4 with 8, 25.8 with 1)
   int ranks = 1;
   while (ranks < 8 && sh.num_seqs * ranks <= 148 && sh.vocab / ranks > 4096) ranks *= 2;
   auto vec_ok = [](const float* x, int64_t stride) {
@@ -730,10 +853,13 @@ cudaError_t launch_verify_draft(const VerifyShape& sh, int32_t* out_tokens, int3
   };
   const bool vec = vec_ok(target, sh.target_stride) && (draft == nullptr || vec_ok(draft, sh.draft_stride));
   auto kernel = vec ? verify_draft_kernel<true> : verify_draft_kernel<false>;
+  const int smem = (vec ? kVerifyRing : 0) + sh.max_query_len * 24;
+  static std::atomic<unsigned long long> configured[2] = {{0}, {0}};
+  if ((e = ensure_smem(kernel, kVerifyRing + kMaxVerifyRows * 24, configured[vec])) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sh.num_seqs) * ranks);
   cfg.blockDim = dim3(kVerifyThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(sh.max_query_len) * 24;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

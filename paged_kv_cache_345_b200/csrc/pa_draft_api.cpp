@@ -16,8 +16,6 @@ int cuda_fail(const char* what, cudaError_t e) {
   return pa_fail(PA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-constexpr int kMaxVerifyRows = 1024;  // rows of a sequence whose facts fit the kernel's shared memory
-
 }  // namespace
 
 extern "C" {
@@ -131,7 +129,7 @@ int pa_decode_tree(void* out, const void* q, const void* k_cache, const void* v_
     return pa_fail(PA_ERR_UNSUPPORTED, "%s: cache larger than 1 TiB", me);
   // units of one sequence (64-key tiles x KV heads x items of 128 rows), and a CTA's
   // share of all, fit 31 bits
-  const int64_t seq_units = (static_cast<int64_t>(max_blocks_per_seq) * block_size / 64 + 1) *
+  const int64_t seq_units = (static_cast<int64_t>(max_blocks_per_seq) * block_size / 64 + 8) *
                             num_kv_heads * ((static_cast<int64_t>(max_query_len) * group + 127) / 128);
   if (seq_units > 0x7fffffff || seq_units > int64_t(0x7fffffff) * 64 / num_seqs)
     return pa_fail(PA_ERR_UNSUPPORTED, "%s: contexts of %lld tokens by %d rows are too large", me,
@@ -180,8 +178,8 @@ int pa_verify_draft(int32_t* out_tokens, int32_t* out_path, int32_t* out_len,
     return pa_fail(PA_ERR_INVALID, "%s: null pointer", me);
   if (vocab_size <= 0 || vocab_size > (1 << 24))
     return pa_fail(PA_ERR_INVALID, "%s: vocab_size %d outside [1, 2^24]", me, vocab_size);
-  if (max_query_len > kMaxVerifyRows)
-    return pa_fail(PA_ERR_UNSUPPORTED, "%s: max_query_len %d > %d", me, max_query_len, kMaxVerifyRows);
+  if (max_query_len > pa::kMaxVerifyRows)
+    return pa_fail(PA_ERR_UNSUPPORTED, "%s: max_query_len %d > %d", me, max_query_len, pa::kMaxVerifyRows);
   if (num_seqs > (1 << 24)) return pa_fail(PA_ERR_UNSUPPORTED, "%s: num_seqs > 2^24", me);
   if (total_q > 1 && (target_stride < vocab_size || (draft_probs && draft_stride < vocab_size)))
     return pa_fail(PA_ERR_INVALID, "%s: a stride is shorter than vocab_size", me);

@@ -128,6 +128,7 @@ cudaError_t launch_qk_norm_rope_append(const QkRowsShape& sh, void* q_out, const
                                        void* v_cache, const float* k_scale, const float* v_scale,
                                        cudaStream_t stream);
 
+constexpr int kMaxVerifyRows = 1024;  // rows of a sequence whose facts pa_verify_draft keeps on chip
 // Sizes of one pa_verify_draft call after validation.
 struct VerifyShape {
   int64_t target_stride, draft_stride;  // floats between rows
@@ -154,13 +155,13 @@ struct TreeShape {
 // Byte offsets of the regions of a pa_decode_tree workspace.
 struct TreeWorkspace {
   size_t ml_off, acc_off, total;
-  int slots;      // partial results (two a CTA)
+  int slots;      // partial results (two a pipeline)
   int slot_rows;  // rows of one
 };
-// Query tiles of 128 rows a CTA of the tree kernel takes at once (1 or 2), and
-// its CTAs.
+// Query tiles of 128 rows a pipeline of the tree kernel takes at once (1 or 2),
+// and its pipelines (over all CTAs).
 int tree_query_tiles(int num_heads, int num_kv_heads, int max_query_len);
-int tree_ctas(int query_tiles);
+int tree_pipelines(int query_tiles);
 TreeWorkspace tree_workspace(int num_heads, int num_kv_heads, int head_dim, int max_query_len);
 cudaError_t launch_decode_tree(const TreeShape& sh, void* out, const void* q, const void* k_cache,
                                const void* v_cache, const int32_t* block_tables,

@@ -11,7 +11,7 @@
 // head of the group), the keys of a 64-key tile the N side.
 //
 // Work is counted in units, one 64-key tile for one KV head and one item of
-// query rows (QT tiles of 128), ordered by sequence, KV head, item, key. A fixed
+// query rows (QT tiles of 128), and some for the item itself, ordered by sequence, KV head, item, key. A fixed
 // number of CTAs take equal, contiguous runs of units (each finds its own from
 // the context lengths, so that a captured call follows them), whatever the
 // lengths are: a run may end inside one (sequence, head, item) and start inside
@@ -53,7 +53,17 @@ namespace {
 
 constexpr int kTreeKeys = 64;    // keys per tile
 constexpr int kTreeRows = 128;   // rows per query tile
-constexpr int kTreeMinUnits = 2; // least units a CTA takes
+// Starting and ending an item (Q, the first tile's latency, the output) costs a CTA
+// about as much as this many tiles: each item counts that many units more, so that
+// a CTA with several short items takes fewer tiles.
+#ifndef TREE_COST
+#define TREE_COST 3
+#endif
+#ifndef TREE_MIN
+#define TREE_MIN 5
+#endif
+constexpr int kTreeItemCost = TREE_COST;
+constexpr int kTreeMinUnits = TREE_MIN;  // least units a CTA takes
 
 // What one partial result belongs to: rows [0, rows) of an item, whose first
 // output row is out_row, split over CTAs first .. last; first < 0: none.
@@ -85,16 +95,19 @@ struct TreeConfig {
   static constexpr int kGran = kTreeKeys * D * 2;      // one K or V tile
   static constexpr int kGranHalf = kTreeKeys * 128;
   static constexpr int kHalves = D / 64;
-  static constexpr int kNG = QT == 1 ? (D == 128 ? 5 : 10) : (D == 128 ? 10 : 12);
-  static constexpr int kRing = QT * kQBytes;
-  static constexpr int kBars = kRing + kNG * kGran;
-  static constexpr int kNumBars = 2 * kNG + 2 + 6 * QT;
-  static constexpr int kScratch = kBars + kNumBars * 8;  // tensor-memory address, then the work search
+  static constexpr int kPipes = QT == 1 ? 2 : 1;       // pipelines of a CTA
+  static constexpr int kNG = QT == 1 ? (D == 128 ? 5 : 11) : (D == 128 ? 10 : 12);
+  static constexpr int kRing = QT * kQBytes;           // a pipeline's Q, then its ring
+  static constexpr int kPipeBytes = kRing + kNG * kGran;
+  static constexpr int kBars = kPipes * kPipeBytes;
+  static constexpr int kNumBars = 2 * kNG + 2 + 6 * QT;  // of a pipeline
+  static constexpr int kScratch = kBars + kPipes * kNumBars * 8;  // tensor-memory address, work search
   static constexpr int kSmemBytes = kScratch + 256;
-  static constexpr int kThreads = 128 + 128 * QT;
-  static constexpr uint32_t kTmemCols = QT == 1 ? 256 : 512;
-  static_assert(2 * 64 * QT + D * QT <= static_cast<int>(kTmemCols), "S and O fit");
-  static_assert(kSmemBytes <= (QT == 1 ? 115712 : 232448), "CTAs per SM");
+  static constexpr int kPipeThreads = 128 + 128 * QT;
+  static constexpr int kThreads = kPipes * kPipeThreads;
+  static constexpr uint32_t kTmemCols = 512, kPipeCols = 512 / kPipes;
+  static_assert(2 * 64 * QT + D * QT <= static_cast<int>(kPipeCols), "S and O fit");
+  static_assert(kScratch % 8 == 0 && kSmemBytes <= 232448, "one CTA per SM");
 };
 
 __device__ __forceinline__ void tree_tma_3d(uint32_t dst, const CUtensorMap* map, int c0, int c1,
@@ -130,14 +143,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, int item
 }
 
 __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& t) {
-  return static_cast<int64_t>(t.nt) * t.items * p.num_kv_heads;
+  return static_cast<int64_t>(t.nt + (t.nt > 0 ? kTreeItemCost : 0)) * t.items * p.num_kv_heads;
 }
 
 // One run of key tiles of one item. Units count from the CTA's first (a
 // sequence's own fit 31 bits: checked on the host for the longest).
 struct TreeRun {
   int s, q0, n, L, nt, h, row_item, t0, t1;
-  int item_unit;  // the item's first unit
+  int tile_unit;  // the unit of the item's first tile
 };
 
 // Calls f(run) for each run of the units [0, units), from sequence s on, whose
@@ -148,9 +161,10 @@ __device__ __forceinline__ void tree_runs(const TreeParams& p, int units, int s,
   int u = 0;
   while (u < units && s < p.num_seqs) {
     const TreeSeq t = tree_seq(p, s, item_tokens);
-    const int own = t.nt * t.items * p.num_kv_heads;
+    const int own = static_cast<int>(tree_units(p, t));
+    const int w = t.nt + kTreeItemCost;  // units of an item: its cost, then its tiles
     while (u < units && u - base < own) {
-      const unsigned item = static_cast<unsigned>(u - base) / static_cast<unsigned>(t.nt);
+      const unsigned item = static_cast<unsigned>(u - base) / static_cast<unsigned>(w);
       TreeRun r;
       r.s = s;
       r.q0 = t.q0;
@@ -159,11 +173,11 @@ __device__ __forceinline__ void tree_runs(const TreeParams& p, int units, int s,
       r.nt = t.nt;
       r.h = t.items == 1 ? item : item / static_cast<unsigned>(t.items);
       r.row_item = static_cast<int>(item) - r.h * t.items;
-      r.item_unit = base + static_cast<int>(item) * t.nt;
-      r.t0 = u - r.item_unit;
-      r.t1 = min(t.nt, r.t0 + (units - u));
-      if (!f(r)) return;
-      u += r.t1 - r.t0;
+      r.tile_unit = base + static_cast<int>(item) * w + kTreeItemCost;
+      r.t0 = max(0, u - r.tile_unit);
+      r.t1 = min(t.nt, units - r.tile_unit);
+      if (r.t1 > r.t0 && !f(r)) return;
+      u = r.tile_unit + t.nt;
     }
     base += own;
     ++s;
@@ -185,27 +199,31 @@ struct RingPos {
 };
 
 template <int D, int QT>
-__global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     pa_tree_kernel(const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map, const TreeParams p) {
   using Cfg = TreeConfig<D, QT>;
   constexpr int NG = Cfg::kNG, KEYN = kTreeKeys, HALVES = Cfg::kHalves;
   extern __shared__ __align__(1024) uint8_t sm[];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::kBars);
+  const int pipe = Cfg::kPipes == 1 ? 0 : static_cast<int>(threadIdx.x) / Cfg::kPipeThreads;
+  const int tid = static_cast<int>(threadIdx.x) - pipe * Cfg::kPipeThreads;  // of the pipeline
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::kBars) + pipe * Cfg::kNumBars;
   auto bar = [&](int i) { return smem_u32(bars + i); };
   // barriers: a granule full, empty; Q full, empty; per query tile and parity of
   // the tile count: S full, P full, P V done
   constexpr int kFull = 0, kEmpty = NG, kQFull = 2 * NG, kQEmpty = 2 * NG + 1, kS = 2 * NG + 2;
   constexpr int kP = kS + 2 * QT, kO = kP + 2 * QT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::kScratch);
-  int64_t* s_sum = reinterpret_cast<int64_t*>(sm + Cfg::kScratch + 16);  // [12]: one a warp
-  int* s_base = reinterpret_cast<int*>(s_sum + 13);
-  int* s_seq = s_base + 1;
-  auto q_s = [&](int x) { return smem_u32(sm + x * Cfg::kQBytes); };
-  auto gran = [&](int st) { return smem_u32(sm + Cfg::kRing) + st * Cfg::kGran; };
+  int64_t* s_sum = reinterpret_cast<int64_t*>(sm + Cfg::kScratch + 16);  // [16]: one a warp
+  int* s_base = reinterpret_cast<int*>(s_sum + 16);                      // [2], then [2]
+  int* s_seq = s_base + 2;
+  const uint32_t pipe_s = smem_u32(sm) + pipe * Cfg::kPipeBytes;
+  auto q_s = [&](int x) { return pipe_s + x * Cfg::kQBytes; };
+  auto gran = [&](int st) { return pipe_s + Cfg::kRing + st * Cfg::kGran; };
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = tid >> 5, lane = threadIdx.x & 31;  // (warp of the pipeline)
+  const int cta_warp = threadIdx.x >> 5;
   const int G = 1 << p.lg_group, TOK = kTreeRows >> p.lg_group;
   const int item_tokens = QT * TOK;
   const int bs = p.block_size, lg = p.log2_block_size;
@@ -217,7 +235,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
     if (threadIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT);
     return;
   }
-  if (threadIdx.x == 0) {
+  if (tid == 0) {
     for (int i = 0; i < NG; ++i) {
       mbar_init(bar(kFull + i), 1);
       mbar_init(bar(kEmpty + i), 1);
@@ -230,11 +248,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
       mbar_init(bar(kO + i), 1);
     }
     fence_barrier_init();
-    prefetch_tensormap(&q_map);
-    prefetch_tensormap(&k_map);
-    prefetch_tensormap(&v_map);
   }
-  if (warp == 2) tc::tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   pdl_wait();  // inputs may come from the previous kernel in the stream
   pdl_launch_dependents();
 
@@ -257,38 +271,46 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
     const int64_t v = __shfl_up_sync(kFullMask, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) s_sum[warp] = incl;
-  if (threadIdx.x == 0) *s_seq = p.num_seqs;
+  if (lane == 31) s_sum[cta_warp] = incl;
+  if (tid == 0) s_seq[pipe] = p.num_seqs;
   __syncthreads();
+  if (cta_warp == 2) tc::tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     const int64_t v = s_sum[w];
-    if (w < warp) incl += v;
+    if (w < cta_warp) incl += v;
     total += v;
   }
-  int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  const unsigned pipes = gridDim.x * Cfg::kPipes;
+  const int64_t most = total + pipes - 1;
+  int64_t share = most < 0xffffffffll ? static_cast<unsigned>(most) / pipes : most / pipes;
   if (share < kTreeMinUnits) share = kTreeMinUnits;
-  const int64_t u0 = blockIdx.x * share;
+  const int me = static_cast<int>(blockIdx.x) * Cfg::kPipes + pipe;  // this pipeline among all
+  const int64_t u0 = me * share;
   const int units = static_cast<int>(max(static_cast<int64_t>(0), min(share, total - u0)));
-  if (units > 0 && incl - own <= u0 && u0 < incl) {
-    int64_t at = incl - own;
-    for (int s = sa; s < sb; ++s) {
-      const int64_t n = tree_units(p, tree_seq(p, s, item_tokens));
-      if (u0 < at + n) {
-        *s_seq = s;
-        *s_base = static_cast<int>(at - u0);
-        break;
+#pragma unroll
+  for (int q = 0; q < Cfg::kPipes; ++q) {
+    const int64_t first = (static_cast<int64_t>(blockIdx.x) * Cfg::kPipes + q) * share;
+    if (incl - own <= first && first < incl) {
+      int64_t at = incl - own;
+      for (int s = sa; s < sb; ++s) {
+        const int64_t n = tree_units(p, tree_seq(p, s, item_tokens));
+        if (first < at + n) {
+          s_seq[q] = s;
+          s_base[q] = static_cast<int>(at - first);
+          break;
+        }
+        at += n;
       }
-      at += n;
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  const int seq0 = *s_seq;
-  const int base0 = *s_base;
+  const uint32_t tmem = *tmem_slot + pipe * Cfg::kPipeCols;
+  const int seq0 = s_seq[pipe];
+  const int base0 = s_base[pipe];
   auto t_s = [&](int x, int b) { return tmem + (2 * x + b) * KEYN; };
   auto t_o = [&](int x) { return tmem + 2 * QT * KEYN + x * D; };
   auto runs = [&](auto&& f) {
@@ -298,6 +320,10 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
   if (warp < 2) {
     // ------------------------------------------------- producers: K and Q, V
     const CUtensorMap* map = warp == 0 ? &k_map : &v_map;
+    if (lane == 0 && units > 0) {
+      prefetch_tensormap(map);
+      if (warp == 0) prefetch_tensormap(&q_map);
+    }
     const int rows = bs < KEYN ? bs : KEYN, lgr = bs < KEYN ? lg : 6;  // tokens per box
     RingPos pos{warp, 0};
     uint32_t qph = 0;
@@ -435,7 +461,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
     TreeHeader none{};
     none.first = -1;
     const bool teller = warp == 4 && lane == 0;
-    TreeHeader* hdr = p.hdr + 2 * blockIdx.x;
+    TreeHeader* hdr = p.hdr + 2 * me;
     if (teller) hdr[0] = hdr[1] = none;
     runs([&](const TreeRun& r) {
       const int my_tok = r.row_item * item_tokens + x * TOK + tok;  // token of this sequence's n
@@ -489,24 +515,29 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
                 if (!((bits >> i) & 1)) sv[32 * c + i] = 0xff800000u;  // -inf
             }
           }
-          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float mx4[4];
 #pragma unroll
-          for (int i = 0; i < KEYN; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(sv[i]));
+          for (int i = 0; i < 4; ++i) mx4[i] = fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 4]));
+#pragma unroll
+          for (int i = 8; i < KEYN; i += 2)
+            mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(sv[i]), __uint_as_float(sv[i + 1]));
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * qs;
           const bool move = mx > m_use + 8.0f;
           const float m_new = move ? mx : m_use;
           alpha = move ? exp2_fast(m_use - m_new) : 1.0f;
           // a row that has seen no key yet keeps m = -inf and weights of 0
-          const float m_sub = m_new == -INFINITY ? 0.0f : m_new;
-          float rs0 = 0.0f, rs1 = 0.0f;
+          const float m_sub = m_new == -INFINITY ? 0.0f : -m_new;
+          const uint64_t q2 = pair_of(qs, qs), m2 = pair_of(m_sub, m_sub);
+          uint64_t rs = 0;
 #pragma unroll
           for (int e = 0; e < KEYN / 2; ++e) {
-            const float a = exp2_fast(fmaf(__uint_as_float(sv[2 * e]), qs, -m_sub));
-            const float b = exp2_fast(fmaf(__uint_as_float(sv[2 * e + 1]), qs, -m_sub));
-            pw[e] = pack_bf16x2(a, b);
-            rs0 += __uint_as_float(pw[e] << 16);
-            rs1 += __uint_as_float(pw[e] & 0xffff0000u);
+            float a, b;
+            floats_of(fma2(pair_of(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), q2, m2), a, b);
+            pw[e] = pack_bf16x2(exp2_fast(a), exp2_fast(b));
+            rs = add2(rs, pair_of(__uint_as_float(pw[e] << 16), __uint_as_float(pw[e] & 0xffff0000u)));
           }
+          float rs0, rs1;
+          floats_of(rs, rs0, rs1);
           l_run = l_run * alpha + (rs0 + rs1);
           m_use = m_new;
         }
@@ -561,38 +592,41 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
         const int64_t base = (static_cast<int64_t>(r.q0) + r.row_item * item_tokens + x * TOK) * p.num_heads +
                              (r.h << p.lg_group);
         if (QT == 1 && p.slot_rows <= 64) {
-          // Q's rows 64 .. 127 hold nothing: 32 rows a warp pass through there (16-byte
-          // pieces swizzled by row), so that the stores are whole rows
-          const uint32_t half0 = q_s(0) + 64 * 128;
-          auto piece = [&](int row, int c) {  // of this warp's 32 rows
-            const int o = (wq * 32 + row) * D * 2 + ((c ^ (row & 7)) << 4);
-            return half0 + (o >> 13) * Cfg::kQHalf + (o & 8191);
-          };
+          // Q's rows 64 .. 127 hold nothing: a warp's 32 rows pass through there (8 KB,
+          // 16-byte pieces swizzled by row), so that the stores are whole rows
+          const uint32_t mine = q_s(0) + 64 * 128 + (D == 128 ? wq * Cfg::kQHalf : wq * 4096);
+          const uint32_t row_at = mine + lane * D * 2;
+          const int sw = (lane & 7) << 4;
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t ov[32];
-            tc::ld32_wait(t_o(x) + lane_off + c * 32, ov);
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t ov[64];
+            tc::ld64_wait(t_o(x) + lane_off + c * 64, ov);
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const uint32_t w0 = pack_bf16x2(__uint_as_float(ov[8 * v]) * inv, __uint_as_float(ov[8 * v + 1]) * inv);
-              const uint32_t w1 = pack_bf16x2(__uint_as_float(ov[8 * v + 2]) * inv, __uint_as_float(ov[8 * v + 3]) * inv);
-              const uint32_t w2 = pack_bf16x2(__uint_as_float(ov[8 * v + 4]) * inv, __uint_as_float(ov[8 * v + 5]) * inv);
-              const uint32_t w3 = pack_bf16x2(__uint_as_float(ov[8 * v + 6]) * inv, __uint_as_float(ov[8 * v + 7]) * inv);
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(piece(lane, c * 4 + v)),
-                           "r"(w0), "r"(w1), "r"(w2), "r"(w3)
+            for (int v = 0; v < 8; ++v) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = pack_bf16x2(__uint_as_float(ov[8 * v + 2 * i]) * inv, __uint_as_float(ov[8 * v + 2 * i + 1]) * inv);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(row_at + (((c * 8 + v) << 4) ^ sw)),
+                           "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                            : "memory");
             }
           }
           __syncwarp();
-          constexpr int kPieces = D / 8, kPer = 32 / kPieces;  // 16-byte pieces a row, rows a store
-          const int left = (r.n - r.row_item * item_tokens) << p.lg_group;  // rows of the item from here on
+          // a store takes kPer rows: row i kPer + (lane / kPieces), piece lane % kPieces
+          constexpr int kPieces = D / 8, kPer = 32 / kPieces;
+          const int sub = lane / kPieces, c = lane % kPieces;
+          const uint32_t from = mine + sub * D * 2;
+          const int left = ((r.n - r.row_item * item_tokens) << p.lg_group) - wq * 32;  // rows from this warp's on
+          __nv_bfloat16* dst = p.out + base * D + c * 8;
+          const int skip = (p.num_heads - G) * D;  // elements between the rows of two tokens, beyond a row
 #pragma unroll
           for (int i = 0; i < 32 / kPer; ++i) {
-            const int row = i * kPer + lane / kPieces, c = lane % kPieces, rr = wq * 32 + row;
-            const uint4 w = lds128(piece(row, c));
-            if (rr < left)
-              *reinterpret_cast<uint4*>(p.out + (base + static_cast<int64_t>(rr >> p.lg_group) * p.num_heads +
-                                                 (rr & (G - 1))) * D + c * 8) = w;
+            const int row = i * kPer + sub;
+            const uint4 w = lds128(from + i * kPer * D * 2 + ((c ^ ((i * kPer + sub) & 7)) << 4));
+            const int rr = wq * 32 + row;
+            if (row < left)
+              *reinterpret_cast<uint4*>(dst + rr * D + static_cast<int64_t>(rr >> p.lg_group) * skip) = w;
           }
           __syncwarp();
         } else {
@@ -617,7 +651,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
       } else {
         // a part of an item: [D / 4][rows][4] so that a warp's stores are whole lines
         const int side = r.t0 > 0 ? 0 : 1;
-        const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + side;
+        const int64_t slot = 2 * static_cast<int64_t>(me) + side;
         const int row = x * kTreeRows + r_;
         if (real) {
           p.ws_ml[slot * p.slot_rows + row] = make_float2(m_use, l_run);
@@ -639,8 +673,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
           const int tok0 = r.row_item * item_tokens;
           hd.out_row = (static_cast<int64_t>(r.q0) + tok0) * p.num_heads + (r.h << p.lg_group);
           hd.rows = min(item_tokens, r.n - tok0) << p.lg_group;
-          hd.first = static_cast<int>((u0 + r.item_unit) / share);
-          hd.last = static_cast<int>((u0 + r.item_unit + r.nt - 1) / share);
+          hd.first = static_cast<int>((u0 + r.tile_unit) / share);
+          hd.last = static_cast<int>((u0 + r.tile_unit + r.nt - 1) / share);
           hdr[side] = hd;
         }
       }
@@ -652,7 +686,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, QT == 1 ? 2 : 1)
 
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 2) tc::tmem_dealloc(tmem, Cfg::kTmemCols);
+  if (cta_warp == 2) tc::tmem_dealloc(*tmem_slot, Cfg::kTmemCols);
 }
 
 // Merge of the items that were split:
@@ -800,11 +834,11 @@ cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* 
   if ((e = encode_tree_q(&qmap, q, sh.total_q, sh.num_heads, D, 1 << p.lg_group, p.q_box_tokens)) != cudaSuccess) return e;
   if ((e = encode_tree_kv(&kmap, k_cache, sh, rows)) != cudaSuccess) return e;
   if ((e = encode_tree_kv(&vmap, v_cache, sh, rows)) != cudaSuccess) return e;
-  const unsigned ctas = static_cast<unsigned>(tree_ctas(QT));
-  e = launch_pdl(pa_tree_kernel<D, QT>, dim3(ctas), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
+  const unsigned parts = static_cast<unsigned>(tree_pipelines(QT));
+  e = launch_pdl(pa_tree_kernel<D, QT>, dim3(parts / Cfg::kPipes), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
                  qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_merge_kernel<D>, dim3(2 * ctas), dim3(kMergeWarps * 32), 0, stream, p);
+  return launch_pdl(tree_merge_kernel<D>, dim3(2 * parts), dim3(kMergeWarps * 32), 0, stream, p);
 }
 
 }  // namespace
@@ -814,18 +848,18 @@ int tree_query_tiles(int num_heads, int num_kv_heads, int max_query_len) {
   return rows > kTreeRows ? 2 : 1;
 }
 
-int tree_ctas(int query_tiles) { return query_tiles == 1 ? 2 * 148 : 148; }
+int tree_pipelines(int query_tiles) { return query_tiles == 1 ? 2 * 148 : 148; }
 
 TreeWorkspace tree_workspace(int num_heads, int num_kv_heads, int head_dim, int max_query_len) {
   TreeWorkspace w{};
   const int qt = tree_query_tiles(num_heads, num_kv_heads, max_query_len);
   const int64_t rows = static_cast<int64_t>(max_query_len) * (num_heads / num_kv_heads);
-  w.slots = 2 * tree_ctas(qt);
+  w.slots = 2 * tree_pipelines(qt);
   // (grows with max_query_len: a workspace for more rows serves fewer)
   w.slot_rows = qt == 2 ? 2 * kTreeRows : static_cast<int>((rows + 31) / 32 * 32);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   const size_t each = static_cast<size_t>(w.slots) * w.slot_rows;
-  w.ml_off = up(static_cast<size_t>(2 * tree_ctas(1)) * sizeof(TreeHeader));
+  w.ml_off = up(static_cast<size_t>(2 * tree_pipelines(1)) * sizeof(TreeHeader));
   w.acc_off = w.ml_off + up(each * sizeof(float2));
   w.total = w.acc_off + each * head_dim * sizeof(float);
   return w;
