@@ -10,28 +10,29 @@
 // bytes. The rows are the M side of the MMA (a tile of 128, row = token * G +
 // head of the group), the keys of a 64-key tile the N side.
 //
-// Work is counted in units, one 64-key tile for one KV head and one item of
-// query rows (QT tiles of 128), and some for the item itself, ordered by sequence, KV head, item, key. A fixed
-// number of CTAs take equal, contiguous runs of units (each finds its own from
-// the context lengths, so that a captured call follows them), whatever the
-// lengths are: a run may end inside one (sequence, head, item) and start inside
-// another. A run that holds all key tiles of its item writes the output;
-// otherwise (m, l, O) go to the workspace (two slots a CTA: the item it starts
-// inside, and the item it ends inside) with a header, and the merge kernel
-// combines the parts of an item in key order. So the result depends on the
-// lengths of the batch (which set the cuts), not on placement or block size.
+// Work is counted in units: one 64-key tile for one KV head and one item of
+// query rows (QT tiles of 128), and a few for each item itself; ordered by
+// sequence, KV head, item, key. A fixed number of pipelines take equal,
+// contiguous stretches of units (each finds its own from the context lengths, so
+// that a captured call follows them), whatever the lengths are: a stretch may end
+// inside one (sequence, head, item) and start inside another. A run that holds
+// all key tiles of its item writes the output; otherwise (m, l, O) go to the
+// workspace (two slots a pipeline: the item it starts inside, and the item it
+// ends inside) with a header, and the merge kernel combines the parts of an item
+// in key order. So the result depends on the lengths of the batch (which set the
+// cuts), not on placement or block size.
 //
-// One CTA:
+// One CTA per SM, of one pipeline (QT = 2: each K/V tile is read once for 256
+// rows) or of two (QT = 1: two streams of loads and two softmaxes hide each
+// other's latency). A pipeline:
 //  * warp 0 / warp 1 (producers): K (and Q) / V tiles by TMA, boxes of {64
-//    columns, min(block_size, 64) tokens} with the 128-byte swizzle, into one
-//    ring of 64-key granules (K, V, K, V, ...), running ahead across items.
+//    columns, min(block_size, 64) tokens} with the 128-byte swizzle, into a
+//    ring of 64-key tiles each, running ahead across items.
 //  * warp 2: S_x = Q_x K^T (M 128, N 64), two tiles ahead; warp 3: O_x += P_x V.
 //  * 4 QT softmax warps, thread = row: as in the prefill kernel (base-2
 //    exponentials against a reference that moves when exceeded by 2^8, P in
 //    tensor memory over its S). P is rounded to bf16 (the type of V), and the row
 //    sum adds the rounded weights, so that they sum to 1 exactly.
-// QT = 1 fits two CTAs on an SM (two streams of loads and two softmaxes to hide
-// each other's latency); QT = 2 reads each K/V tile once for 256 rows.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
@@ -53,9 +54,9 @@ namespace {
 
 constexpr int kTreeKeys = 64;    // keys per tile
 constexpr int kTreeRows = 128;   // rows per query tile
-// Starting and ending an item (Q, the first tile's latency, the output) costs a CTA
-// about as much as this many tiles: each item counts that many units more, so that
-// a CTA with several short items takes fewer tiles.
+// Starting and ending an item (Q, the first tile's latency, the output) costs about
+// as much as this many tiles: each item counts that many units more, so that a
+// pipeline with several short items takes fewer tiles.
 #ifndef TREE_COST
 #define TREE_COST 3
 #endif
@@ -63,10 +64,10 @@ constexpr int kTreeRows = 128;   // rows per query tile
 #define TREE_MIN 5
 #endif
 constexpr int kTreeItemCost = TREE_COST;
-constexpr int kTreeMinUnits = TREE_MIN;  // least units a CTA takes
+constexpr int kTreeMinUnits = TREE_MIN;  // least units a pipeline takes
 
 // What one partial result belongs to: rows [0, rows) of an item, whose first
-// output row is out_row, split over CTAs first .. last; first < 0: none.
+// output row is out_row, split over pipelines first .. last; first < 0: none.
 struct TreeHeader {
   int64_t out_row;
   int rows, first, last, pad[3];
@@ -79,9 +80,9 @@ struct TreeParams {
   const int32_t* query_start;
   const int32_t* parents;
   unsigned* err;
-  TreeHeader* hdr;  // [CTAs][2]
-  float2* ws_ml;    // [CTAs][2][slot_rows]: reference maximum, sum
-  float* ws_acc;    // [CTAs][2][D / 4][slot_rows][4]
+  TreeHeader* hdr;  // [pipelines][2]
+  float2* ws_ml;    // [pipelines][2][slot_rows]: reference maximum, sum
+  float* ws_acc;    // [pipelines][2][D / 4][slot_rows][4]
   int num_heads, num_kv_heads, lg_group, block_size, log2_block_size, num_blocks;
   int max_blocks_per_seq, num_seqs, total_q, max_query_len, slot_rows;
   int q_box_tokens;  // tokens of a query tile that are loaded
@@ -96,8 +97,13 @@ struct TreeConfig {
   static constexpr int kGranHalf = kTreeKeys * 128;
   static constexpr int kHalves = D / 64;
   static constexpr int kPipes = QT == 1 ? 2 : 1;       // pipelines of a CTA
-  static constexpr int kNG = QT == 1 ? (D == 128 ? 5 : 11) : (D == 128 ? 10 : 12);
-  static constexpr int kRing = QT * kQBytes;           // a pipeline's Q, then its ring
+  // K and V tiles in flight. Two rings, each with one producer: its wait for a tile
+  // to be free can then never be a whole phase ahead of its barrier (in one ring
+  // that both producers filled in turns it could, when a commit came late).
+  static constexpr int kNK = QT == 1 ? (D == 128 ? 2 : 5) : (D == 128 ? 5 : 6);
+  static constexpr int kNV = QT == 1 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 6);
+  static constexpr int kNG = kNK + kNV;
+  static constexpr int kRing = QT * kQBytes;           // a pipeline's Q, then its K and V rings
   static constexpr int kPipeBytes = kRing + kNG * kGran;
   static constexpr int kBars = kPipes * kPipeBytes;
   static constexpr int kNumBars = 2 * kNG + 2 + 6 * QT;  // of a pipeline
@@ -146,7 +152,7 @@ __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq
   return static_cast<int64_t>(t.nt + (t.nt > 0 ? kTreeItemCost : 0)) * t.items * p.num_kv_heads;
 }
 
-// One run of key tiles of one item. Units count from the CTA's first (a
+// One run of key tiles of one item. Units count from the pipeline's first (a
 // sequence's own fit 31 bits: checked on the host for the longest).
 struct TreeRun {
   int s, q0, n, L, nt, h, row_item, t0, t1;
@@ -184,15 +190,16 @@ __device__ __forceinline__ void tree_runs(const TreeParams& p, int units, int s,
   }
 }
 
-// A place in the ring of granules: its index and the parity of its use.
+// A place in a ring of N tiles from `first` on, and the parity of its use.
+template <int N>
 struct RingPos {
   int st;
   uint32_t ph;
-  template <int NG>
-  __device__ __forceinline__ void step2() {  // two granules on
-    st += 2;
-    if (st >= NG) {
-      st -= NG;
+  int first;
+  __device__ __forceinline__ explicit RingPos(int first_) : st(first_), ph(0), first(first_) {}
+  __device__ __forceinline__ void step() {
+    if (++st == first + N) {
+      st = first;
       ph ^= 1;
     }
   }
@@ -204,13 +211,13 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
                    const __grid_constant__ CUtensorMap k_map,
                    const __grid_constant__ CUtensorMap v_map, const TreeParams p) {
   using Cfg = TreeConfig<D, QT>;
-  constexpr int NG = Cfg::kNG, KEYN = kTreeKeys, HALVES = Cfg::kHalves;
+  constexpr int NK = Cfg::kNK, NV = Cfg::kNV, NG = Cfg::kNG, KEYN = kTreeKeys, HALVES = Cfg::kHalves;
   extern __shared__ __align__(1024) uint8_t sm[];
   const int pipe = Cfg::kPipes == 1 ? 0 : static_cast<int>(threadIdx.x) / Cfg::kPipeThreads;
   const int tid = static_cast<int>(threadIdx.x) - pipe * Cfg::kPipeThreads;  // of the pipeline
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::kBars) + pipe * Cfg::kNumBars;
   auto bar = [&](int i) { return smem_u32(bars + i); };
-  // barriers: a granule full, empty; Q full, empty; per query tile and parity of
+  // barriers: a tile (K's, then V's) full, empty; Q full, empty; per query tile and parity of
   // the tile count: S full, P full, P V done
   constexpr int kFull = 0, kEmpty = NG, kQFull = 2 * NG, kQEmpty = 2 * NG + 1, kS = 2 * NG + 2;
   constexpr int kP = kS + 2 * QT, kO = kP + 2 * QT;
@@ -248,11 +255,17 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       mbar_init(bar(kO + i), 1);
     }
     fence_barrier_init();
+    if (pipe == 0) {  // descriptors are kernel parameters: fetch them early
+      prefetch_tensormap(&q_map);
+      prefetch_tensormap(&k_map);
+      prefetch_tensormap(&v_map);
+    }
   }
+  if (cta_warp == 2) tc::tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   pdl_wait();  // inputs may come from the previous kernel in the stream
   pdl_launch_dependents();
 
-  // The units of the batch, then this CTA's run and the sequence it starts in:
+  // The units of the batch, then each pipeline's stretch and the sequence it starts in:
   // each thread sums its own consecutive sequences, one scan joins the threads,
   // and the thread whose sequences hold the first unit finds the one.
   constexpr int NT = Cfg::kThreads, NW = NT / 32;
@@ -274,7 +287,6 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   if (lane == 31) s_sum[cta_warp] = incl;
   if (tid == 0) s_seq[pipe] = p.num_seqs;
   __syncthreads();
-  if (cta_warp == 2) tc::tmem_alloc(smem_u32(tmem_slot), Cfg::kTmemCols);
   int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
@@ -320,13 +332,10 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   if (warp < 2) {
     // ------------------------------------------------- producers: K and Q, V
     const CUtensorMap* map = warp == 0 ? &k_map : &v_map;
-    if (lane == 0 && units > 0) {
-      prefetch_tensormap(map);
-      if (warp == 0) prefetch_tensormap(&q_map);
-    }
     const int rows = bs < KEYN ? bs : KEYN, lgr = bs < KEYN ? lg : 6;  // tokens per box
-    RingPos pos{warp, 0};
-    uint32_t qph = 0;
+    int st = warp == 0 ? 0 : NK;  // the place in this producer's ring
+    const int first = st, last = warp == 0 ? NK - 1 : NG - 1;
+    uint32_t ph = 0, qph = 0;
     runs([&](const TreeRun& r) {
       if (warp == 0) {
         bool ok = true;
@@ -354,8 +363,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         if (lane < nbox * HALVES) blk = __ldg(trow + ((key0 + b * rows) >> lg));
         bool ok = true;
         if (lane == 0) {
-          ok = mbar_wait(bar(kEmpty + pos.st), pos.ph ^ 1, p.err);
-          if (ok) mbar_arrive_expect_tx(bar(kFull + pos.st), static_cast<uint32_t>(nbox * rows * 128 * HALVES));
+          ok = mbar_wait(bar(kEmpty + st), ph ^ 1, p.err);
+          if (ok) mbar_arrive_expect_tx(bar(kFull + st), static_cast<uint32_t>(nbox * rows * 128 * HALVES));
         }
         if (!__shfl_sync(kFullMask, ok, 0)) return false;
         if (lane < nbox * HALVES) {
@@ -363,17 +372,20 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
           if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks))
             atomicOr(p.err, PA_DEVERR_BLOCK_ID);
           const int half = lane >= nbox;
-          tma_load_4d(gran(pos.st) + half * Cfg::kGranHalf + b * rows * 128, map, half * 64,
-                      (key0 + b * rows) & (bs - 1), r.h, blk, bar(kFull + pos.st));
+          tma_load_4d(gran(st) + half * Cfg::kGranHalf + b * rows * 128, map, half * 64,
+                      (key0 + b * rows) & (bs - 1), r.h, blk, bar(kFull + st));
         }
-        pos.step2<NG>();
+        if (++st > last) {
+          st = first;
+          ph ^= 1;
+        }
       }
       return true;
     });
   } else if (warp == 2) {
     // -------------------------------------------------------- S = Q K^T MMAs
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(kTreeRows, KEYN, 0);
-    RingPos pos{0, 0};
+    RingPos<NK> pos(0);
     uint32_t qph = 0;
     int it = 0;  // tiles so far, over all runs
     bool ended = false;
@@ -404,26 +416,28 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
           if (t == r.t1 - 1) tc::commit(bar(kQEmpty));
         }
         __syncwarp();
-        pos.step2<NG>();
+        pos.step();
       }
       ended = true;
       return true;
     });
-    // The CTA must not leave while a commit is still to arrive on its barriers:
-    // the queue of the tensor pipe, shared with the SM's other CTA, may hold one
-    // back past the last output. The S, P V and Q barriers' last phases are
-    // waited for by their readers; the last of each granule's and of Q's
-    // "empty" have no reader left, so they are waited for here.
+    // The CTA must not leave while a commit is still to arrive on its barriers.
+    // The last phases of "S full" and "P V done" are waited for by their readers;
+    // the last of each K and V place's and of Q's "empty" have no reader left, so
+    // they are waited for here.
+    if (ended && lane < NG) {
+      const int n = lane < NK ? NK : NV, at = lane < NK ? lane : lane - NK;
+      const int uses = (it - at + n - 1) / n;  // of this lane's place
+      if (it > at) mbar_wait(bar(kEmpty + lane), (uses - 1) & 1, p.err);
+    }
     if (ended) {
-      const int uses = (2 * it - lane + NG - 1) / NG;  // of granule `lane`
-      if (lane < NG && 2 * it > lane) mbar_wait(bar(kEmpty + lane), (uses - 1) & 1, p.err);
       mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
       __syncwarp();
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ P V MMAs
     constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
-    RingPos pos{1, 0};
+    RingPos<NV> pos(NK);
     int it = 0;
     runs([&](const TreeRun& r) {
       for (int t = r.t0; t < r.t1; ++t, ++it) {
@@ -444,7 +458,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         }
         if (lane == 0) tc::commit(bar(kEmpty + pos.st));
         __syncwarp();
-        pos.step2<NG>();
+        pos.step();
       }
       return true;
     });
@@ -456,7 +470,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     const int tok = r_ >> p.lg_group, g = r_ & (G - 1);
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const float qs = p.q_scale;
-    RingPos vpos{1, 0};
+    RingPos<NV> vpos(NK);
     int it = 0;
     TreeHeader none{};
     none.first = -1;
@@ -575,7 +589,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        vpos.step2<NG>();
+        vpos.step();
         tc::fence_before_sync();
         mbar_arrive(bar(kP + 2 * x + (it & 1)));
         if (t > r.t0 && !rescale) {
@@ -692,7 +706,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
 // Merge of the items that were split:
 //   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j
 // over all parts j. An item's pieces (32 rows x 4 columns, a lane one row) are
-// dealt to the CTAs that held a part of it. With fewer pieces than warps, W warps
+// dealt to as many CTAs as it has parts. With fewer pieces than warps, W warps
 // share a piece, taking the parts in turn and joining in shared memory in their
 // order; so the sums' order goes by the item's rows and parts alone.
 // Latency-bound: a header, one round trip per kMergeParts W parts.
@@ -731,7 +745,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
           const int jj = j0 + j * W;
           mq[j] = make_float2(-INFINITY, 0.0f);
           if (jj < parts) {
-            // the first part lies in its CTA's second slot, the others in the first
+            // the first part lies in its pipeline's second slot, the others in the first
             const int64_t sl = 2 * static_cast<int64_t>(hd.first + jj) + (jj == 0 ? 1 : 0);
             mq[j] = ld_cg_f32x2(ml + sl * p.slot_rows * 2);
             v[j] = ld_cg_f32x4(av + sl * p.slot_rows * D);
