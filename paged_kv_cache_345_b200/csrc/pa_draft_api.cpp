@@ -127,13 +127,12 @@ int pa_decode_tree(void* out, const void* q, const void* k_cache, const void* v_
   if (static_cast<int64_t>(num_blocks) * block_size * num_kv_heads * head_dim * 2 / 16 >
       (int64_t(1) << 36))
     return pa_fail(PA_ERR_UNSUPPORTED, "%s: cache larger than 1 TiB", me);
-  // units of one sequence (64-key tiles x KV heads x items of 128 rows), and a CTA's
-  // share of all, fit 31 bits
+  // the kernel counts its work (64-key tiles x KV heads x items of 128 rows) in 31 bits
   const int64_t seq_units = (static_cast<int64_t>(max_blocks_per_seq) * block_size / 64 + 8) *
                             num_kv_heads * ((static_cast<int64_t>(max_query_len) * group + 127) / 128);
-  if (seq_units > 0x7fffffff || seq_units > int64_t(0x7fffffff) * 64 / num_seqs)
-    return pa_fail(PA_ERR_UNSUPPORTED, "%s: contexts of %lld tokens by %d rows are too large", me,
-                   static_cast<long long>(max_blocks_per_seq) * block_size, max_query_len);
+  if (seq_units > 0x7fffffff / num_seqs)
+    return pa_fail(PA_ERR_UNSUPPORTED, "%s: %d tables of %lld tokens by %d rows are too large", me,
+                   num_seqs, static_cast<long long>(max_blocks_per_seq) * block_size, max_query_len);
   if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(query_start, 4) ||
       !aligned(parents, 4) || !aligned(workspace, 16))

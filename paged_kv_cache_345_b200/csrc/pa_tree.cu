@@ -57,14 +57,11 @@ constexpr int kTreeRows = 128;   // rows per query tile
 // Starting and ending an item (Q, the first tile's latency, the output) costs about
 // as much as this many tiles: each item counts that many units more, so that a
 // pipeline with several short items takes fewer tiles.
-#ifndef TREE_COST
-#define TREE_COST 3
-#endif
-#ifndef TREE_MIN
-#define TREE_MIN 5
-#endif
-constexpr int kTreeItemCost = TREE_COST;
-constexpr int kTreeMinUnits = TREE_MIN;  // least units a pipeline takes
+constexpr int kTreeItemCost = 2;
+constexpr int kTreeMinUnits = 3;  // least units a pipeline takes
+// An item of at most so many units is not cut: the merge would cost more than the
+// uneven stretches (1,024 sequences of 166 tokens: 239 us cut, 224 whole).
+constexpr int kTreeWhole = 8;
 
 // What one partial result belongs to: rows [0, rows) of an item, whose first
 // output row is out_row, split over pipelines first .. last; first < 0: none.
@@ -148,12 +145,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int s, int item
   return t;
 }
 
-__device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& t) {
-  return static_cast<int64_t>(t.nt + (t.nt > 0 ? kTreeItemCost : 0)) * t.items * p.num_kv_heads;
+// (all sequences' together fit 31 bits: checked on the host for the longest)
+__device__ __forceinline__ int tree_units(const TreeParams& p, const TreeSeq& t) {
+  return (t.nt + (t.nt > 0 ? kTreeItemCost : 0)) * t.items * p.num_kv_heads;
 }
 
-// One run of key tiles of one item. Units count from the pipeline's first (a
-// sequence's own fit 31 bits: checked on the host for the longest).
+// One run of key tiles of one item. Units count from the pipeline's first.
 struct TreeRun {
   int s, q0, n, L, nt, h, row_item, t0, t1;
   int tile_unit;  // the unit of the item's first tile
@@ -167,7 +164,7 @@ __device__ __forceinline__ void tree_runs(const TreeParams& p, int units, int s,
   int u = 0;
   while (u < units && s < p.num_seqs) {
     const TreeSeq t = tree_seq(p, s, item_tokens);
-    const int own = static_cast<int>(tree_units(p, t));
+    const int own = tree_units(p, t);
     const int w = t.nt + kTreeItemCost;  // units of an item: its cost, then its tiles
     while (u < units && u - base < own) {
       const unsigned item = static_cast<unsigned>(u - base) / static_cast<unsigned>(w);
@@ -180,8 +177,14 @@ __device__ __forceinline__ void tree_runs(const TreeParams& p, int units, int s,
       r.h = t.items == 1 ? item : item / static_cast<unsigned>(t.items);
       r.row_item = static_cast<int>(item) - r.h * t.items;
       r.tile_unit = base + static_cast<int>(item) * w + kTreeItemCost;
+      const int from = u - (r.tile_unit - kTreeItemCost), to = units - (r.tile_unit - kTreeItemCost);
       r.t0 = max(0, u - r.tile_unit);
       r.t1 = min(t.nt, units - r.tile_unit);
+      if (w <= kTreeWhole) {
+        // a short item goes whole to the stretch that holds its middle
+        r.t0 = 0;
+        r.t1 = 2 * from < w && 2 * to >= w ? t.nt : 0;
+      }
       if (r.t1 > r.t0 && !f(r)) return;
       u = r.tile_unit + t.nt;
     }
@@ -222,8 +225,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   constexpr int kFull = 0, kEmpty = NG, kQFull = 2 * NG, kQEmpty = 2 * NG + 1, kS = 2 * NG + 2;
   constexpr int kP = kS + 2 * QT, kO = kP + 2 * QT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + Cfg::kScratch);
-  int64_t* s_sum = reinterpret_cast<int64_t*>(sm + Cfg::kScratch + 16);  // [16]: one a warp
-  int* s_base = reinterpret_cast<int*>(s_sum + 16);                      // [2], then [2]
+  int* s_sum = reinterpret_cast<int*>(sm + Cfg::kScratch + 16);  // [16]: one a warp
+  int* s_base = s_sum + 16;                                      // [2], then [2]
   int* s_seq = s_base + 2;
   const uint32_t pipe_s = smem_u32(sm) + pipe * Cfg::kPipeBytes;
   auto q_s = [&](int x) { return pipe_s + x * Cfg::kQBytes; };
@@ -271,46 +274,44 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   constexpr int NT = Cfg::kThreads, NW = NT / 32;
   const int per = (p.num_seqs + NT - 1) / NT;
   const int sa = threadIdx.x * per, sb = min(sa + per, p.num_seqs);
-  int64_t own = 0;
+  int own = 0;
 #pragma unroll 4
   for (int s = sa; s < sb; ++s) {
     const TreeSeq t = tree_seq(p, s, item_tokens);
     if (t.bad && blockIdx.x == 0) atomicOr(p.err, PA_DEVERR_CONTEXT);
     own += tree_units(p, t);
   }
-  int64_t incl = own;
+  int incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(kFullMask, incl, o);
+    const int v = __shfl_up_sync(kFullMask, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) s_sum[cta_warp] = incl;
   if (tid == 0) s_seq[pipe] = p.num_seqs;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const int64_t v = s_sum[w];
+    const int v = s_sum[w];
     if (w < cta_warp) incl += v;
     total += v;
   }
   const unsigned pipes = gridDim.x * Cfg::kPipes;
-  const int64_t most = total + pipes - 1;
-  int64_t share = most < 0xffffffffll ? static_cast<unsigned>(most) / pipes : most / pipes;
-  if (share < kTreeMinUnits) share = kTreeMinUnits;
+  const int share = max(static_cast<int>((static_cast<unsigned>(total) + pipes - 1) / pipes), kTreeMinUnits);
   const int me = static_cast<int>(blockIdx.x) * Cfg::kPipes + pipe;  // this pipeline among all
-  const int64_t u0 = me * share;
-  const int units = static_cast<int>(max(static_cast<int64_t>(0), min(share, total - u0)));
+  const int64_t u0 = static_cast<int64_t>(me) * share;
+  const int units = static_cast<int>(max(static_cast<int64_t>(0), min(static_cast<int64_t>(share), total - u0)));
 #pragma unroll
   for (int q = 0; q < Cfg::kPipes; ++q) {
     const int64_t first = (static_cast<int64_t>(blockIdx.x) * Cfg::kPipes + q) * share;
     if (incl - own <= first && first < incl) {
-      int64_t at = incl - own;
+      int at = incl - own;
       for (int s = sa; s < sb; ++s) {
-        const int64_t n = tree_units(p, tree_seq(p, s, item_tokens));
+        const int n = tree_units(p, tree_seq(p, s, item_tokens));
         if (first < at + n) {
           s_seq[q] = s;
-          s_base[q] = static_cast<int>(at - first);
+          s_base[q] = at - static_cast<int>(first);
           break;
         }
         at += n;
@@ -329,7 +330,13 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     if (units > 0) tree_runs(p, units, seq0, base0, item_tokens, f);
   };
 
+  // Two pipelines: 512 threads launched with 128 registers each; the producers and
+  // issuers hand 56 of theirs to the softmax warpgroups (72 + 184 = 2 * 128).
+  auto fewer = [] {
+    if constexpr (QT == 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+  };
   if (warp < 2) {
+    fewer();
     // ------------------------------------------------- producers: K and Q, V
     const CUtensorMap* map = warp == 0 ? &k_map : &v_map;
     const int rows = bs < KEYN ? bs : KEYN, lgr = bs < KEYN ? lg : 6;  // tokens per box
@@ -337,6 +344,15 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     const int first = st, last = warp == 0 ? NK - 1 : NG - 1;
     uint32_t ph = 0, qph = 0;
     runs([&](const TreeRun& r) {
+      const int32_t* trow = p.block_tables + static_cast<int64_t>(r.s) * p.max_blocks_per_seq;
+      auto boxes = [&](int t) { return (min(KEYN, r.L - t * KEYN) + rows - 1) >> lgr; };  // <= 8
+      // the block of this lane's box of tile t (lanes past the boxes: of the second
+      // half of the columns), read one tile ahead
+      auto entry = [&](int t, int nbox) {
+        const int b = lane < nbox ? lane : lane - nbox;
+        return lane < nbox * HALVES ? __ldg(trow + ((t * KEYN + b * rows) >> lg)) : 0;
+      };
+      int next = entry(r.t0, boxes(r.t0));
       if (warp == 0) {
         bool ok = true;
         if (lane == 0) {
@@ -353,14 +369,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         if (!__shfl_sync(kFullMask, ok, 0)) return false;
         qph ^= 1;
       }
-      const int32_t* trow = p.block_tables + static_cast<int64_t>(r.s) * p.max_blocks_per_seq;
       for (int t = r.t0; t < r.t1; ++t) {
-        const int key0 = t * KEYN;
-        const int nkeys = min(KEYN, r.L - key0);
-        const int nbox = (nkeys + rows - 1) >> lgr;  // <= 8
-        const int b = lane % nbox;
-        int blk = 0;
-        if (lane < nbox * HALVES) blk = __ldg(trow + ((key0 + b * rows) >> lg));
+        const int nbox = boxes(t), blk = next;
+        if (t + 1 < r.t1) next = entry(t + 1, boxes(t + 1));
         bool ok = true;
         if (lane == 0) {
           ok = mbar_wait(bar(kEmpty + st), ph ^ 1, p.err);
@@ -371,9 +382,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
           // an id outside the pool is flagged; TMA reads an out-of-range box as zeros
           if (static_cast<unsigned>(blk) >= static_cast<unsigned>(p.num_blocks))
             atomicOr(p.err, PA_DEVERR_BLOCK_ID);
-          const int half = lane >= nbox;
+          const int half = lane >= nbox, b = half ? lane - nbox : lane;
           tma_load_4d(gran(st) + half * Cfg::kGranHalf + b * rows * 128, map, half * 64,
-                      (key0 + b * rows) & (bs - 1), r.h, blk, bar(kFull + st));
+                      (t * KEYN + b * rows) & (bs - 1), r.h, blk, bar(kFull + st));
         }
         if (++st > last) {
           st = first;
@@ -384,6 +395,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     });
   } else if (warp == 2) {
     // -------------------------------------------------------- S = Q K^T MMAs
+    fewer();
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(kTreeRows, KEYN, 0);
     RingPos<NK> pos(0);
     uint32_t qph = 0;
@@ -401,15 +413,15 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
         tc::fence_after_sync();
         if (lane == 0) {
-          const uint32_t kb = gran(pos.st);
+          // (a k-step's operands lie a constant on: added to the descriptor, in 16 bytes)
+          const uint64_t kd = tc::smem_desc_sw128(gran(pos.st), 16, 1024);
 #pragma unroll
           for (int x = 0; x < QT; ++x) {
+            const uint64_t qd = tc::smem_desc_sw128(q_s(x), 16, 1024);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks)
-              tc::mma_bf16(t_s(x, it & 1),
-                           tc::smem_desc_sw128(q_s(x) + (ks >> 2) * Cfg::kQHalf + (ks & 3) * 32, 16, 1024),
-                           tc::smem_desc_sw128(kb + (ks >> 2) * Cfg::kGranHalf + (ks & 3) * 32, 16, 1024),
-                           kIdS, ks > 0);
+              tc::mma_bf16(t_s(x, it & 1), qd + (((ks >> 2) * Cfg::kQHalf + (ks & 3) * 32) >> 4),
+                           kd + (((ks >> 2) * Cfg::kGranHalf + (ks & 3) * 32) >> 4), kIdS, ks > 0);
             tc::commit(bar(kS + 2 * x + (it & 1)));
           }
           tc::commit(bar(kEmpty + pos.st));
@@ -436,21 +448,21 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ P V MMAs
+    fewer();
     constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
     RingPos<NV> pos(NK);
     int it = 0;
     runs([&](const TreeRun& r) {
       for (int t = r.t0; t < r.t1; ++t, ++it) {
         if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
-        const uint32_t vb = gran(pos.st);
+        const uint64_t vd = tc::smem_desc_sw128(gran(pos.st), Cfg::kGranHalf, 1024);
         for (int x = 0; x < QT; ++x) {
           if (!wait_all(bar(kP + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
           tc::fence_after_sync();
           if (lane == 0) {
 #pragma unroll
             for (int ks = 0; ks < KEYN / 16; ++ks)
-              tc::mma_bf16_tmem_a(t_o(x), t_s(x, it & 1) + ks * 8,
-                                  tc::smem_desc_sw128(vb + ks * 2048, Cfg::kGranHalf, 1024), kIdPV,
+              tc::mma_bf16_tmem_a(t_o(x), t_s(x, it & 1) + ks * 8, vd + ((ks * 2048) >> 4), kIdPV,
                                   t > r.t0 || ks > 0);
             tc::commit(bar(kO + 2 * x + (it & 1)));
           }
@@ -464,6 +476,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     });
   } else {
     // -------------------------------------------------------------- softmax
+    if constexpr (QT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     const int x = (warp - 4) >> 2;  // query tile of this warpgroup
     const int wq = warp & 3;        // tensor-memory lanes 32 wq .. 32 wq + 31
     const int r_ = wq * 32 + lane;  // row
@@ -477,6 +490,16 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     const bool teller = warp == 4 && lane == 0;
     TreeHeader* hdr = p.hdr + 2 * me;
     if (teller) hdr[0] = hdr[1] = none;
+    // Up to 64 rows an item, warps wq = 2, 3 have no rows: they store the outputs
+    // that warps 0, 1 leave in shared memory (barriers "there" and "taken", 64
+    // threads), while those go on with the next run.
+    const bool relay = QT == 1 && p.slot_rows <= 64;
+    const int there = 1 + pipe * 4 + (wq & 1) * 2, taken = there + 1;
+    bool left_some = false, failed = false;
+    auto fail = [&] {  // a wait gave up
+      failed = true;
+      return false;
+    };
     runs([&](const TreeRun& r) {
       const int my_tok = r.row_item * item_tokens + x * TOK + tok;  // token of this sequence's n
       const bool real = my_tok < r.n;
@@ -489,7 +512,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       if (p.parents != nullptr && real) parent = __ldg(p.parents + r.q0 + my_tok);
       float m_use = -INFINITY, l_run = 0.0f;
       for (int t = r.t0; t < r.t1; ++t, ++it) {
-        if (!wait_all(bar(kS + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
+        if (!wait_all(bar(kS + 2 * x + (it & 1)), (it >> 1) & 1)) return fail();
         tc::fence_after_sync();
         const int key0 = t * KEYN;
         float alpha = 1.0f;
@@ -557,7 +580,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         }
         const bool rescale = t > r.t0 && __any_sync(kFullMask, alpha != 1.0f);
         if (rescale) {
-          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return false;
+          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return fail();
           tc::fence_after_sync();
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
@@ -576,7 +599,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         if (x == 0 && key0 + KEYN > r.L) {
           // keys past the context: stale or unwritten V rows become zeros (their
           // P is 0, but 0 * NaN would not be)
-          if (!wait_all(bar(kFull + vpos.st), vpos.ph)) return false;
+          if (!wait_all(bar(kFull + vpos.st), vpos.ph)) return fail();
           const int nkeys = r.L - key0;
           const uint32_t vb = gran(vpos.st);
           constexpr int kVecs = 8 * HALVES;
@@ -593,23 +616,53 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         tc::fence_before_sync();
         mbar_arrive(bar(kP + 2 * x + (it & 1)));
         if (t > r.t0 && !rescale) {
-          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return false;
+          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return fail();
         }
       }
       // the run's end: O of all its tiles
-      if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return false;
+      if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return fail();
       tc::fence_after_sync();
+      const bool whole = r.t0 == 0 && r.t1 == r.nt;
+      // row r_ of the item is output row base + (r_ >> lg_group) * num_heads + its head
+      const int64_t base = (static_cast<int64_t>(r.q0) + r.row_item * item_tokens + x * TOK) * p.num_heads +
+                           (r.h << p.lg_group);
+      // the relay's place: Q's rows 64 .. 127 hold nothing; 32 rows a warp (8 KB, 16-byte
+      // pieces swizzled by row), so that the stores are whole rows
+      const uint32_t place = q_s(0) + 64 * 128 + (D == 128 ? (wq & 1) * Cfg::kQHalf : (wq & 1) * 4096);
+      if (relay && wq >= 2) {
+        const int left = ((r.n - r.row_item * item_tokens) << p.lg_group) - (wq - 2) * 32;  // rows from the warp's on
+        if (!whole || left <= 0) return true;
+        // a store takes kPer rows: row i kPer + (lane / kPieces), piece lane % kPieces
+        constexpr int kPieces = D / 8, kPer = 32 / kPieces, kN = 32 / kPer;
+        const int sub = lane / kPieces, c = lane % kPieces;
+        const uint32_t from = place + sub * D * 2;
+        __nv_bfloat16* dst = p.out + base * D + c * 8;
+        const int skip = (p.num_heads - G) * D;  // elements between the rows of two tokens, beyond a row
+        asm volatile("bar.sync %0, 64;" ::"r"(there) : "memory");
+        uint4 w[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          w[i] = lds128(from + i * kPer * D * 2 + ((c ^ ((i * kPer + sub) & 7)) << 4));
+        asm volatile("bar.arrive %0, 64;" ::"r"(taken) : "memory");
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int row = i * kPer + sub, rr = (wq - 2) * 32 + row;
+          if (row < left)
+            *reinterpret_cast<uint4*>(dst + rr * D + static_cast<int64_t>(rr >> p.lg_group) * skip) = w[i];
+        }
+        return true;
+      }
       if (!warp_real) return true;
-      if (r.t0 == 0 && r.t1 == r.nt) {
+      if (whole) {
         const float inv = 1.0f / l_run;
-        // row r_ of the item is output row base + (r_ >> lg_group) * num_heads + its head
-        const int64_t base = (static_cast<int64_t>(r.q0) + r.row_item * item_tokens + x * TOK) * p.num_heads +
-                             (r.h << p.lg_group);
-        if (QT == 1 && p.slot_rows <= 64) {
-          // Q's rows 64 .. 127 hold nothing: a warp's 32 rows pass through there (8 KB,
-          // 16-byte pieces swizzled by row), so that the stores are whole rows
-          const uint32_t mine = q_s(0) + 64 * 128 + (D == 128 ? wq * Cfg::kQHalf : wq * 4096);
-          const uint32_t row_at = mine + lane * D * 2;
+        if (relay) {
+          if (relay && failed) {  // let the other warp go
+      asm volatile("bar.arrive %0, 64;" ::"r"(wq >= 2 ? taken : there) : "memory");
+    } else if (left_some) {
+      asm volatile("bar.sync %0, 64;" ::"r"(taken) : "memory");
+    }
+          left_some = true;
+          const uint32_t row_at = place + lane * D * 2;
           const int sw = (lane & 7) << 4;
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
@@ -626,23 +679,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
                            : "memory");
             }
           }
-          __syncwarp();
-          // a store takes kPer rows: row i kPer + (lane / kPieces), piece lane % kPieces
-          constexpr int kPieces = D / 8, kPer = 32 / kPieces;
-          const int sub = lane / kPieces, c = lane % kPieces;
-          const uint32_t from = mine + sub * D * 2;
-          const int left = ((r.n - r.row_item * item_tokens) << p.lg_group) - wq * 32;  // rows from this warp's on
-          __nv_bfloat16* dst = p.out + base * D + c * 8;
-          const int skip = (p.num_heads - G) * D;  // elements between the rows of two tokens, beyond a row
-#pragma unroll
-          for (int i = 0; i < 32 / kPer; ++i) {
-            const int row = i * kPer + sub;
-            const uint4 w = lds128(from + i * kPer * D * 2 + ((c ^ ((i * kPer + sub) & 7)) << 4));
-            const int rr = wq * 32 + row;
-            if (row < left)
-              *reinterpret_cast<uint4*>(dst + rr * D + static_cast<int64_t>(rr >> p.lg_group) * skip) = w;
-          }
-          __syncwarp();
+          asm volatile("bar.arrive %0, 64;" ::"r"(there) : "memory");
         } else {
           __nv_bfloat16* dst = p.out + (base + static_cast<int64_t>(tok) * p.num_heads + g) * D;
 #pragma unroll
@@ -696,6 +733,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       // published, which these threads do after the loads above)
       return true;
     });
+    if (left_some) asm volatile("bar.sync %0, 64;" ::"r"(taken) : "memory");
   }
 
   tc::fence_before_sync();
