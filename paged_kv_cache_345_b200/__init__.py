@@ -261,23 +261,22 @@ def _on_device(tensors, stream):
     return torch.cuda.device(dev), _stream(stream, dev)
 
 
-def _call(fn, args, tensors, stream):
-    """fn(*args, stream pointer) on the tensors' device, checked as in _on_device. The
-    usual call, every tensor on the current device, takes a shorter way there."""
-    torch = _torch()
-    if stream is None and torch.cuda.is_initialized():
-        here = torch.cuda.current_device()
-        for t in tensors:
-            if t is not None and t.get_device() != here:
-                break
-        else:
-            status = fn(*args, _stream(None, here))
-            if status != PA_OK:
-                _check(status)
-            return
-    guard, st = _on_device(tensors, stream)
-    with guard:
-        _check(fn(*args, st))
+_native_module = None
+
+
+def _native():
+    """_pa_torch.so: the same checks and calls in C++ (binding/pa_torch.cpp), bound to the
+    functions of the library loaded above. Needs torch, so it is loaded at the first use."""
+    global _native_module
+    if _native_module is None:
+        _torch()
+        from . import _pa_torch
+        names = ("pa_qk_norm_rope_append", "pa_decode_tree", "pa_verify_draft", "pa_kv_accept",
+                 "pa_last_error")
+        _pa_torch.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names},
+                       PagedAttentionError)
+        _native_module = _pa_torch
+    return _native_module
 
 
 # ---------------------------------------------------------------- kernels
@@ -291,11 +290,13 @@ def pa_kv_append(k_new, v_new, slot_mapping, k_cache, v_cache, stream=None) -> N
     if v_cache.shape != k_cache.shape or slot_mapping.shape != (k_new.shape[0],):
         raise ValueError("cache or slot_mapping shape mismatch")
     dt = k_cache.dtype
-    _call(_lib.pa_kv_append, (
-        _dev_ptr(k_new, "k_new", dt), _dev_ptr(v_new, "v_new", dt),
-        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", dt), nb, bs, hkv, d,
-        _dtype_code(k_cache)), (k_new, v_new, slot_mapping, k_cache, v_cache), stream)
+    guard, st = _on_device((k_new, v_new, slot_mapping, k_cache, v_cache), stream)
+    with guard:
+        _check(_lib.pa_kv_append(
+            _dev_ptr(k_new, "k_new", dt), _dev_ptr(v_new, "v_new", dt),
+            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
+            _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", dt), nb, bs, hkv, d,
+            _dtype_code(k_cache), st))
 
 
 def pa_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale,
@@ -313,13 +314,15 @@ def pa_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_sc
         raise TypeError("caches must hold E4M3 codes (uint8 or float8_e4m3fn)")
     if k_scale.shape != (hkv,) or v_scale.shape != (hkv,):
         raise ValueError("k_scale/v_scale must be [num_kv_heads]")
-    _call(_lib.pa_kv_append_fp8, (
-        _dev_ptr(k_new, "k_new", torch.bfloat16), _dev_ptr(v_new, "v_new", torch.bfloat16),
-        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-        _dev_ptr(k_scale, "k_scale", torch.float32),
-        _dev_ptr(v_scale, "v_scale", torch.float32), nb, bs, hkv, d),
-        (k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale), stream)
+    guard, st = _on_device((k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale),
+                           stream)
+    with guard:
+        _check(_lib.pa_kv_append_fp8(
+            _dev_ptr(k_new, "k_new", torch.bfloat16), _dev_ptr(v_new, "v_new", torch.bfloat16),
+            _dev_ptr(slot_mapping, "slot_mapping", torch.int64), k_new.shape[0],
+            _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
+            _dev_ptr(k_scale, "k_scale", torch.float32),
+            _dev_ptr(v_scale, "v_scale", torch.float32), nb, bs, hkv, d, st))
 
 
 def pa_copy_blocks(k_cache, v_cache, block_mapping, stream=None) -> None:
@@ -721,21 +724,6 @@ def pa_prefill_plan(query_start, context_lens, num_heads: int, num_kv_heads: int
     return out[:n.value]
 
 
-def _dev_rows(t, name, dtype):
-    """(pointer, elements between tokens) of a [N, heads, d] view whose heads are
-    dense: a contiguous tensor, or one part of a packed projection."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = t.shape
-    st = t.stride()
-    if (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
-        if t.numel():
-            raise ValueError(f"{name} must be [N, heads, head_dim] with dense heads")
-    return t.data_ptr(), (st[0] if n > 1 else h * d)
-
-
 def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin,
                            q_weight=None, k_weight=None, eps: float = 1e-6,
                            interleaved: bool = False, k_scale=None, v_scale=None,
@@ -747,41 +735,9 @@ def pa_qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_c
     apart (q_out may be q); positions: int32 [N]; slot_mapping: int64 [N];
     cos_sin: float32 [max_position, rotary_dim], cosines then sines; k_scale,
     v_scale: with E4M3 caches. See pa_qk_norm_rope_append in include/pa.h."""
-    torch = _torch()
-    nb, bs, hkv, d = k_cache.shape
-    fp8 = _is_fp8(k_cache)
-    dt = torch.bfloat16 if fp8 else k_cache.dtype
-    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != d or k.shape[2] != d or \
-            q_out.shape != q.shape or v.shape != k.shape or k.shape[0] != q.shape[0] or \
-            k.shape[1] != hkv:
-        raise ValueError("q/q_out must be [N, num_heads, head_dim], k/v [N, num_kv_heads, head_dim]")
-    n, hq = q.shape[:2]
-    if v_cache.shape != k_cache.shape or positions.shape != (n,) or slot_mapping.shape != (n,):
-        raise ValueError("cache, positions or slot_mapping shape mismatch")
-    if cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be [max_position, rotary_dim]")
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and w.shape != (d,):
-            raise ValueError(f"{name} must be [head_dim]")
-    if fp8 != (k_scale is not None) or (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale go with (and only with) E4M3 caches")
-    if fp8 and (k_scale.shape != (hkv,) or v_scale.shape != (hkv,)):
-        raise ValueError("k_scale/v_scale must be [num_kv_heads]")
-    (po, so), (pq, sq) = _dev_rows(q_out, "q_out", dt), _dev_rows(q, "q", dt)
-    (pk, sk), (pv, sv) = _dev_rows(k, "k", dt), _dev_rows(v, "v", dt)
-    f32 = torch.float32
-    _call(_lib.pa_qk_norm_rope_append, (
-        po, pq, pk, pv, so, sq, sk, sv, _dev_ptr(positions, "positions", torch.int32),
-        _dev_ptr(slot_mapping, "slot_mapping", torch.int64), n, _dev_ptr(cos_sin, "cos_sin", f32),
-        *cos_sin.shape, 1 if interleaved else 0,
-        None if q_weight is None else _dev_ptr(q_weight, "q_weight", dt),
-        None if k_weight is None else _dev_ptr(k_weight, "k_weight", dt), float(eps),
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", k_cache.dtype),
-        None if k_scale is None else _dev_ptr(k_scale, "k_scale", f32),
-        None if v_scale is None else _dev_ptr(v_scale, "v_scale", f32), nb, bs, hq, hkv, d,
-        _dtype_code(k_cache)),
-        (q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin, q_weight, k_weight,
-         k_scale, v_scale), stream)
+    _native().qk_norm_rope_append(q_out, q, k, v, positions, slot_mapping, k_cache, v_cache,
+                                  cos_sin, q_weight, k_weight, eps, interleaved, k_scale, v_scale,
+                                  stream)
 
 
 def pa_decode_tree_workspace_bytes(num_heads, num_kv_heads, head_dim, max_query_len) -> int:
@@ -799,40 +755,8 @@ def pa_decode_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_s
     [S], the rows counted; parents: int32 [total_q] or None; workspace: a uint8
     CUDA tensor of at least pa_decode_tree_workspace_bytes(...) bytes. See
     pa_decode_tree in include/pa.h."""
-    torch = _torch()
-    nb, bs, hkv, d = k_cache.shape
-    total_q, hq, dq = q.shape
-    s = context_lens.shape[0]
-    if dq != d or out.shape != q.shape or v_cache.shape != k_cache.shape:
-        raise ValueError("q/out/cache shape mismatch")
-    if block_tables.dim() != 2 or block_tables.shape[0] != s or query_start.shape != (s + 1,):
-        raise ValueError("block_tables must be [S, max_blocks], query_start [S + 1]")
-    if parents is not None and parents.shape != (total_q,):
-        raise ValueError("parents must be [total_q]")
-    if workspace is None:
-        raise ValueError("pa_decode_tree needs a workspace")
-    dt, i32 = k_cache.dtype, torch.int32
-    _call(_lib.pa_decode_tree, (
-        _dev_ptr(out, "out", dt), _dev_ptr(q, "q", dt), _dev_ptr(k_cache, "k_cache"),
-        _dev_ptr(v_cache, "v_cache", dt), _dev_ptr(block_tables, "block_tables", i32),
-        _dev_ptr(context_lens, "context_lens", i32), _dev_ptr(query_start, "query_start", i32),
-        None if parents is None else _dev_ptr(parents, "parents", i32), s, total_q, hq, hkv, d, bs,
-        nb, block_tables.shape[1], int(max_query_len), float(scale), _dev_ptr(workspace, "workspace"),
-        workspace.nbytes, _dtype_code(k_cache)),
-        (out, q, k_cache, v_cache, block_tables, context_lens, query_start, parents, workspace),
-        stream)
-
-
-def _prob_rows(t, name, rows, vocab):
-    """(pointer, floats between rows) of a float32 [rows, vocab] tensor with dense rows."""
-    torch = _torch()
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != torch.float32:
-        raise TypeError(f"{name} must be {torch.float32}, got {t.dtype}")
-    if tuple(t.shape) != (rows, vocab) or (vocab > 1 and t.numel() and t.stride(1) != 1):
-        raise ValueError(f"{name} must be [total_q, vocab_size] with dense rows")
-    return t.data_ptr(), (t.stride(0) if rows > 1 else vocab)
+    _native().decode_tree(out, q, k_cache, v_cache, block_tables, context_lens, query_start,
+                          parents, max_query_len, scale, workspace, stream)
 
 
 def pa_verify_draft(out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens,
@@ -845,31 +769,8 @@ def pa_verify_draft(out_tokens, out_path, out_len, target_probs, draft_probs, dr
     row stride; draft_tokens, parents (or None: chains): int32 [total_q];
     query_start: int32 [S + 1]; u_accept: float32 [total_q], u_sample: float32
     [S]. See pa_verify_draft in include/pa.h."""
-    torch = _torch()
-    if out_tokens.dim() != 2 or out_path.shape != out_tokens.shape:
-        raise ValueError("out_tokens and out_path must be [S, max_query_len]")
-    if target_probs.dim() != 2:
-        raise ValueError("target_probs must be [total_q, vocab_size]")
-    s, most = out_tokens.shape
-    total_q, vocab = target_probs.shape
-    if out_len.shape != (s,) or query_start.shape != (s + 1,) or u_sample.shape != (s,):
-        raise ValueError("out_len and u_sample must be [S], query_start [S + 1]")
-    for t, name in ((draft_tokens, "draft_tokens"), (u_accept, "u_accept"), (parents, "parents")):
-        if t is not None and t.shape != (total_q,):
-            raise ValueError(f"{name} must be [total_q]")
-    i32, f32 = torch.int32, torch.float32
-    pt, ts = _prob_rows(target_probs, "target_probs", total_q, vocab)
-    pd, ds = (None, 0) if draft_probs is None else \
-        _prob_rows(draft_probs, "draft_probs", total_q, vocab)
-    _call(_lib.pa_verify_draft, (
-        _dev_ptr(out_tokens, "out_tokens", i32), _dev_ptr(out_path, "out_path", i32),
-        _dev_ptr(out_len, "out_len", i32), pt, ts, pd, ds,
-        _dev_ptr(draft_tokens, "draft_tokens", i32),
-        None if parents is None else _dev_ptr(parents, "parents", i32),
-        _dev_ptr(query_start, "query_start", i32), _dev_ptr(u_accept, "u_accept", f32),
-        _dev_ptr(u_sample, "u_sample", f32), s, total_q, vocab, most),
-        (out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens, parents,
-         query_start, u_accept, u_sample), stream)
+    _native().verify_draft(out_tokens, out_path, out_len, target_probs, draft_probs, draft_tokens,
+                           parents, query_start, u_accept, u_sample, stream)
 
 
 def pa_kv_accept(k_cache, v_cache, block_tables, context_lens, query_start, path, path_len,
@@ -880,23 +781,8 @@ def pa_kv_accept(k_cache, v_cache, block_tables, context_lens, query_start, path
     path: int32 [S, max_path_len], path_len: int32 [S] (pa_verify_draft's out_path
     and out_len); the rest as in the step's pa_decode_tree. See pa_kv_accept in
     include/pa.h."""
-    torch = _torch()
-    nb, bs, hkv, d = k_cache.shape
-    s = context_lens.shape[0]
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("cache shape mismatch")
-    if block_tables.dim() != 2 or block_tables.shape[0] != s or query_start.shape != (s + 1,):
-        raise ValueError("block_tables must be [S, max_blocks], query_start [S + 1]")
-    if path.dim() != 2 or path.shape[0] != s or path_len.shape != (s,):
-        raise ValueError("path must be [S, max_path_len], path_len [S]")
-    i32 = torch.int32
-    _call(_lib.pa_kv_accept, (
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache", k_cache.dtype),
-        _dev_ptr(block_tables, "block_tables", i32), _dev_ptr(context_lens, "context_lens", i32),
-        _dev_ptr(query_start, "query_start", i32), _dev_ptr(path, "path", i32),
-        _dev_ptr(path_len, "path_len", i32), s, path.shape[1], nb, bs, block_tables.shape[1], hkv,
-        d, _dtype_code(k_cache)),
-        (k_cache, v_cache, block_tables, context_lens, query_start, path, path_len), stream)
+    _native().kv_accept(k_cache, v_cache, block_tables, context_lens, query_start, path, path_len,
+                        stream)
 
 
 def pa_device_errors(stream=None) -> int:

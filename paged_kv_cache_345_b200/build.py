@@ -1,10 +1,11 @@
-"""Build libpa.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Build libpa.so (the C-ABI library) in-tree with nvcc for sm_100a, and
+_pa_torch.so (argument marshalling from torch tensors) with the host compiler.
 
 Usage: python paged_kv_cache_345_b200/build.py [--force] [--verbose]
 (run it by path: importing the package first would load the library.)
-The shared library lands next to this file; objects go to _build/ at the
+The shared libraries land next to this file; objects go to _build/ at the
 repository root. A rebuild happens only when a source or header is newer than
-the library (or with --force).
+the libraries (or with --force).
 """
 
 from __future__ import annotations
@@ -23,6 +24,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+BINDING = os.path.join(PKG, "binding", "pa_torch.cpp")
+BINDING_LIB = os.path.join(PKG, "_pa_torch.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3,-Wall",
@@ -46,10 +49,32 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING_LIB):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _inputs())
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING_LIB))
+    return all(os.path.getmtime(p) <= t for p in [*_inputs(), BINDING])
+
+
+def _build_binding() -> None:
+    """Compile the torch binding against the installed torch and Python headers."""
+    import sysconfig
+
+    import torch
+
+    base = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-Wno-unknown-pragmas", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), BINDING, "-o", tmp,
+           "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(BINDING)}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING_LIB)
 
 
 def _compile(src: str, verbose: bool) -> str:
@@ -66,12 +91,14 @@ def _compile(src: str, verbose: bool) -> str:
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile every CUDA/C++ source of the library and link libpa.so."""
+    """Compile every CUDA/C++ source of the library, link libpa.so, build the binding."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(lambda s: _compile(s, verbose), sources()))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [_nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread",
            "-lrt"]
