@@ -271,8 +271,8 @@ def _native():
     if _native_module is None:
         _torch()
         from . import _pa_torch
-        names = ("pa_qk_norm_rope_append", "pa_decode_tree", "pa_verify_draft", "pa_kv_accept",
-                 "pa_last_error")
+        names = ("pa_kv_append", "pa_kv_append_fp8", "pa_qk_norm_rope_append", "pa_decode_tree",
+                 "pa_verify_draft", "pa_kv_accept", "pa_last_error")
         _pa_torch.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names},
                        PagedAttentionError)
         _native_module = _pa_torch
@@ -283,6 +283,8 @@ def _native():
 
 def pa_kv_append(k_new, v_new, slot_mapping, k_cache, v_cache, stream=None) -> None:
     """Write row i of k_new/v_new [N, Hkv, d] at flat slot slot_mapping[i] (int64) of the caches."""
+    if k_cache.is_cuda:
+        return _native().kv_append(k_new, v_new, slot_mapping, k_cache, v_cache, stream)
     torch = _torch()
     nb, bs, hkv, d = k_cache.shape
     if tuple(k_new.shape[1:]) != (hkv, d) or k_new.shape != v_new.shape:
@@ -304,6 +306,9 @@ def pa_kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_sc
     """Quantising append into E4M3 caches (uint8 codes [nb, bs, Hkv, d]): row i of
     k_new/v_new (bfloat16 [N, Hkv, d]) goes to flat slot slot_mapping[i] as the codes
     of value / scale[head]; k_scale/v_scale are float32 [Hkv] device tensors."""
+    if k_cache.is_cuda:
+        return _native().kv_append_fp8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale,
+                                       v_scale, stream)
     torch = _torch()
     nb, bs, hkv, d = k_cache.shape
     if tuple(k_new.shape[1:]) != (hkv, d) or k_new.shape != v_new.shape:

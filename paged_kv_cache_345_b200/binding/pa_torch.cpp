@@ -1,5 +1,5 @@
-// Argument marshalling of the calls of a decode step with drafted tokens, in C++:
-// from torch tensors straight to the C ABI (include/pa.h). The Python functions of
+// Argument marshalling of the cache writes and of the calls of a decode step with
+// drafted tokens, in C++: from torch tensors straight to the C ABI (include/pa.h). The Python functions of
 // the package carry the signatures and documentation and pass their arguments on
 // in order; what they check is checked here, with the same exceptions (ValueError,
 // TypeError, PagedAttentionError). Small calls are bound by this: the rows of a
@@ -24,6 +24,8 @@
 namespace {
 
 struct Bound {
+  decltype(&::pa_kv_append) kv_append;
+  decltype(&::pa_kv_append_fp8) kv_append_fp8;
   decltype(&::pa_qk_norm_rope_append) qk_norm_rope_append;
   decltype(&::pa_decode_tree) decode_tree;
   decltype(&::pa_verify_draft) verify_draft;
@@ -196,6 +198,46 @@ PyObject* guarded(const char* name, Py_ssize_t got, Py_ssize_t want, F&& f) {
   Py_RETURN_NONE;
 }
 
+// k_new, v_new, slot_mapping, k_cache, v_cache, stream
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("kv_append", n, 6, [&] {
+    Call c;
+    const Cache kv = caches(c, a[3], a[4]);
+    const at::ScalarType dt = kv.k.scalar_type();
+    const at::Tensor& k = c.tensor(a[0], "k_new", dt);
+    const at::Tensor& v = c.tensor(a[1], "v_new", dt);
+    const at::Tensor& slots = c.tensor(a[2], "slot_mapping", at::kLong);
+    if (k.dim() != 3 || k.size(1) != kv.hkv || k.size(2) != kv.d || v.sizes() != k.sizes())
+      raise(PyExc_ValueError, "k_new/v_new must be [N, num_kv_heads, head_dim] matching the cache");
+    if (!shaped(slots, {k.size(0)})) raise(PyExc_ValueError, "cache or slot_mapping shape mismatch");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
+    call(lib.kv_append, at_(k), at_(v), to<int64_t>(slots), narrow(k.size(0), "num_tokens"), at_(kv.k), at_(kv.v),
+         kv.nb, kv.bs, kv.hkv, kv.d, kv.type, c.stream(a[5]));
+  });
+}
+
+// k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_scale, stream
+PyObject* kv_append_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded("kv_append_fp8", n, 8, [&] {
+    Call c;
+    const Cache kv = caches(c, a[3], a[4]);
+    if (kv.type != PA_FP8_E4M3) raise(PyExc_TypeError, "caches must hold E4M3 codes (uint8 or float8_e4m3fn)");
+    const at::Tensor& k = c.tensor(a[0], "k_new", at::kBFloat16);
+    const at::Tensor& v = c.tensor(a[1], "v_new", at::kBFloat16);
+    const at::Tensor& slots = c.tensor(a[2], "slot_mapping", at::kLong);
+    if (k.dim() != 3 || k.size(1) != kv.hkv || k.size(2) != kv.d || v.sizes() != k.sizes())
+      raise(PyExc_ValueError, "k_new/v_new must be [N, num_kv_heads, head_dim] matching the cache");
+    if (!shaped(slots, {k.size(0)})) raise(PyExc_ValueError, "cache or slot_mapping shape mismatch");
+    const at::Tensor& ks = c.tensor(a[5], "k_scale", at::kFloat);
+    const at::Tensor& vs = c.tensor(a[6], "v_scale", at::kFloat);
+    if (!shaped(ks, {kv.hkv}) || !shaped(vs, {kv.hkv}))
+      raise(PyExc_ValueError, "k_scale/v_scale must be [num_kv_heads]");
+    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
+    call(lib.kv_append_fp8, at_(k), at_(v), to<int64_t>(slots), narrow(k.size(0), "num_tokens"), at_(kv.k),
+         at_(kv.v), to<float>(ks), to<float>(vs), kv.nb, kv.bs, kv.hkv, kv.d, c.stream(a[7]));
+  });
+}
+
 // q_out, q, k, v, positions, slot_mapping, k_cache, v_cache, cos_sin, q_weight, k_weight,
 // eps, interleaved, k_scale, v_scale, stream
 PyObject* qk_norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -230,11 +272,12 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int interleaved = PyObject_IsTrue(a[12]);
     if (interleaved < 0) throw Raised{};
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
-    call(lib.qk_norm_rope_append, at_(out), at_(q), at_(k), at_(v), c.rows(out, "q_out"), c.rows(q, "q"), c.rows(k, "k"), c.rows(v, "v"),
-        to<int32_t>(pos), to<int64_t>(slots), narrow(q.size(0), "num_tokens"), to<float>(cs),
-        narrow(cs.size(0), "max_position"), narrow(cs.size(1), "rotary_dim"), interleaved, at_(qw), at_(kw),
-        static_cast<float>(number(a[11])), at_(kv.k), at_(kv.v), to<float>(ks), to<float>(vs), kv.nb, kv.bs,
-        narrow(q.size(1), "num_heads"), kv.hkv, kv.d, kv.type, c.stream(a[15]));
+    call(lib.qk_norm_rope_append, at_(out), at_(q), at_(k), at_(v), c.rows(out, "q_out"), c.rows(q, "q"),
+         c.rows(k, "k"), c.rows(v, "v"),
+         to<int32_t>(pos), to<int64_t>(slots), narrow(q.size(0), "num_tokens"), to<float>(cs),
+         narrow(cs.size(0), "max_position"), narrow(cs.size(1), "rotary_dim"), interleaved, at_(qw), at_(kw),
+         static_cast<float>(number(a[11])), at_(kv.k), at_(kv.v), to<float>(ks), to<float>(vs), kv.nb, kv.bs,
+         narrow(q.size(1), "num_heads"), kv.hkv, kv.d, kv.type, c.stream(a[15]));
   });
 }
 
@@ -260,10 +303,10 @@ PyObject* decode_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& ws = c.tensor(a[10], "workspace");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
     call(lib.decode_tree, at_(out), at_(q), at_(kv.k), at_(kv.v), to<int32_t>(tables), to<int32_t>(lens),
-                          to<int32_t>(start), to<int32_t>(parents), narrow(lens.size(0), "num_seqs"),
-                          narrow(q.size(0), "total_q"), narrow(q.size(1), "num_heads"), kv.hkv, kv.d, kv.bs, kv.nb,
-                          narrow(tables.size(1), "max_blocks_per_seq"), narrow(whole(a[8]), "max_query_len"),
-                          static_cast<float>(number(a[9])), at_(ws), ws.nbytes(), kv.type, c.stream(a[11]));
+         to<int32_t>(start), to<int32_t>(parents), narrow(lens.size(0), "num_seqs"),
+         narrow(q.size(0), "total_q"), narrow(q.size(1), "num_heads"), kv.hkv, kv.d, kv.bs, kv.nb,
+         narrow(tables.size(1), "max_blocks_per_seq"), narrow(whole(a[8]), "max_query_len"),
+         static_cast<float>(number(a[9])), at_(ws), ws.nbytes(), kv.type, c.stream(a[11]));
   });
 }
 
@@ -300,9 +343,9 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t ts = stride(target, "target_probs"), ds = draft ? stride(*draft, "draft_probs") : 0;
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
     call(lib.verify_draft, to<int32_t>(out), to<int32_t>(path), to<int32_t>(len), to<float>(target), ts,
-                           to<float>(draft), ds, to<int32_t>(tokens), to<int32_t>(parents), to<int32_t>(start),
-                           to<float>(ua), to<float>(us), narrow(s, "num_seqs"), narrow(rows, "total_q"),
-                           narrow(vocab, "vocab_size"), narrow(out.size(1), "max_query_len"), c.stream(a[10]));
+         to<float>(draft), ds, to<int32_t>(tokens), to<int32_t>(parents), to<int32_t>(start),
+         to<float>(ua), to<float>(us), narrow(s, "num_seqs"), narrow(rows, "total_q"),
+         narrow(vocab, "vocab_size"), narrow(out.size(1), "max_query_len"), c.stream(a[10]));
   });
 }
 
@@ -322,9 +365,9 @@ PyObject* kv_accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
       raise(PyExc_ValueError, "path must be [S, max_path_len], path_len [S]");
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
     call(lib.kv_accept, at_(kv.k), at_(kv.v), to<int32_t>(tables), to<int32_t>(lens), to<int32_t>(start),
-                        to<int32_t>(path), to<int32_t>(len), narrow(lens.size(0), "num_seqs"),
-                        narrow(path.size(1), "max_path_len"), kv.nb, kv.bs,
-                        narrow(tables.size(1), "max_blocks_per_seq"), kv.hkv, kv.d, kv.type, c.stream(a[7]));
+         to<int32_t>(path), to<int32_t>(len), narrow(lens.size(0), "num_seqs"),
+         narrow(path.size(1), "max_path_len"), kv.nb, kv.bs,
+         narrow(tables.size(1), "max_blocks_per_seq"), kv.hkv, kv.d, kv.type, c.stream(a[7]));
   });
 }
 
@@ -343,7 +386,8 @@ PyObject* bind(PyObject*, PyObject* args) {
     fn = reinterpret_cast<std::remove_reference_t<decltype(fn)>>(static_cast<uintptr_t>(at));
     return true;
   };
-  if (!take("pa_qk_norm_rope_append", lib.qk_norm_rope_append) || !take("pa_decode_tree", lib.decode_tree) ||
+  if (!take("pa_kv_append", lib.kv_append) || !take("pa_kv_append_fp8", lib.kv_append_fp8) ||
+      !take("pa_qk_norm_rope_append", lib.qk_norm_rope_append) || !take("pa_decode_tree", lib.decode_tree) ||
       !take("pa_verify_draft", lib.verify_draft) || !take("pa_kv_accept", lib.kv_accept) ||
       !take("pa_last_error", lib.last_error))
     return nullptr;
@@ -357,6 +401,8 @@ PyCFunction method(F f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<
 
 PyMethodDef methods[] = {
     {"bind", bind, METH_VARARGS, nullptr},
+    {"kv_append", method(kv_append), METH_FASTCALL, nullptr},
+    {"kv_append_fp8", method(kv_append_fp8), METH_FASTCALL, nullptr},
     {"qk_norm_rope_append", method(qk_norm_rope_append), METH_FASTCALL, nullptr},
     {"decode_tree", method(decode_tree), METH_FASTCALL, nullptr},
     {"verify_draft", method(verify_draft), METH_FASTCALL, nullptr},
