@@ -6,6 +6,8 @@
 // block; here a step writes several per sequence and keeps some of them.
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
+#include <utility>
 
 #include <cooperative_groups.h>
 
@@ -435,6 +437,7 @@ struct VerifyParams {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWarps = kVerifyThreads / 32;
+constexpr int kVerifyPart = 8 * kVerifyWarps / 32;  // a lane's share of a cluster's sums
 constexpr int kVerifyBatch = 4;  // groups of 128 values that a warp takes at once
 constexpr int kVerifyChunk = 128 * kVerifyBatch;
 constexpr int kVerifyStages = 3;  // of a warp's ring: a chunk of p and one of q each
@@ -454,9 +457,101 @@ struct Residual {
   int gone;  // picked drafts: rejected tokens so far (their list is in shared memory)
 };
 
-__device__ __forceinline__ double mass_of(float p, float q, double t) {
-  const double r = static_cast<double>(p) - t * (q > 0.0f ? static_cast<double>(q) : 0.0);
-  return r > 0.0 ? r : 0.0;  // (NaN: 0)
+// A float >= 0 as a double times 2^-896: its bits three places down, which holds for
+// zero and subnormals too (an infinity becomes 2^128 2^-896). Two shifts, where the
+// conversion instruction goes at a quarter of the rate of float64 arithmetic (measured:
+// 16 to 62 a clock and SM).
+__device__ __forceinline__ double scaled(float x) {
+  const unsigned u = __float_as_uint(x);
+  return __hiloint2double(static_cast<int>(u >> 3), static_cast<int>(u << 29));
+}
+constexpr double kUnscale = 0x1p896;
+
+// sum += m where m > 0 (NaN: not), as one predicated addition.
+__device__ __forceinline__ void add_positive(double& sum, double m) {
+  asm("{\n .reg .pred p;\n setp.gt.f64 p, %1, 0d0000000000000000;\n @p add.f64 %0, %0, %1;\n}"
+      : "+d"(sum)
+      : "d"(m));
+}
+
+// Where a running sum over a warp's values (lane-major, N a lane, on top of `run`)
+// first passes `want`: the index and the sum before it; index -1: nowhere. The same for
+// the last value above 0. `run` then counts them all.
+struct Passed {
+  int first, last;
+  double first_before, last_before;
+};
+template <int N>
+__device__ __forceinline__ Passed find_passed(const double (&m)[N], double want, double& run, int lane) {
+  double c[N];
+  c[0] = m[0];
+#pragma unroll
+  for (int e = 1; e < N; ++e) c[e] = c[e - 1] + m[e];
+  double incl = c[N - 1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double t = __shfl_up_sync(kFullMask, incl, o);
+    if (lane >= o) incl += t;
+  }
+  const double base = run + (incl - c[N - 1]);
+  int hit = N, end = -1;
+  double hit_before = 0.0, end_before = 0.0;
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (!(m[e] > 0.0)) continue;
+    const double before = e == 0 ? base : base + c[e - 1];
+    if (hit == N && base + c[e] > want) {
+      hit = e;
+      hit_before = before;
+    }
+    end = e;
+    end_before = before;
+  }
+  const unsigned hits = __ballot_sync(kFullMask, hit < N), ends = __ballot_sync(kFullMask, end >= 0);
+  const int hl = hits ? __ffs(hits) - 1 : 0, el = ends ? 31 - __clz(ends) : 0;
+  Passed r;
+  r.first = __shfl_sync(kFullMask, lane * N + hit, hl);
+  r.first_before = __shfl_sync(kFullMask, hit_before, hl);
+  r.last = __shfl_sync(kFullMask, lane * N + end, el);
+  r.last_before = __shfl_sync(kFullMask, end_before, el);
+  if (!hits) r.first = -1;
+  if (!ends) r.last = -1;
+  run += __shfl_sync(kFullMask, incl, 31);
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cluster_address(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// A double into another CTA's shared memory, counted as 8 bytes by its mbarrier.
+__device__ __forceinline__ void store_async(uint32_t addr, double v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %1, [%2];" ::"r"(addr),
+               "l"(__double_as_longlong(v)), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+// As mbar_wait, for what other CTAs of the cluster stored.
+__device__ __forceinline__ void mbar_wait_cluster(uint32_t bar, uint32_t parity, unsigned* err) {
+  if (mbar_try_wait_cluster(bar, parity)) return;
+  const uint64_t start = global_timer_ns();
+  while (!mbar_try_wait_cluster(bar, parity)) {
+    if (global_timer_ns() - start > kWaitLimitNs) {
+      atomicOr(err, PA_DEVERR_TIMEOUT);
+      return;
+    }
+  }
 }
 
 // One cluster of CTAs per sequence. Every CTA walks the rows in order with the
@@ -465,25 +560,31 @@ __device__ __forceinline__ double mass_of(float p, float q, double t) {
 // token read up front by one thread. Sums over the vocabulary are split over
 // the cluster's warps, a contiguous piece each, in 64 bits: a sampled draft's
 // mass only when a later child is tried, and the last token's at the end, whose
-// piece is then searched. All in float64. Bound by reading one row of p and one of
-// q per sequence, and by their passes from L2 for further children.
+// piece is then searched. All in float64. The bytes are one row of p and one of q per
+// sequence; what bounds it are the sums of a sequence, one after the other: each
+// needs the one before (about 2.4 us each over 128,256 values, of which the walk's and
+// the exchange's latency is a third). 64 trees of 16 over 128,256 values: 36.6 us;
+// one chain of 5 over 32,000: 6.8 us; 256 plain draws (p alone, 131 MB): 28 us.
 template <bool VEC>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = static_cast<int>(cluster.block_rank()), ranks = static_cast<int>(cluster.num_blocks());
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  // the warps' rings; per row p(token), q(token), u, token, parent; then the
-  // rejected tokens' list
+  // the warps' rings; per row p(token), q(token), u q(token), token, parent; then
+  // the rejected tokens' list
   const int cap = p.max_query_len;
-  float* s_p = reinterpret_cast<float*>(smem_raw + (VEC ? kVerifyRing : 0));
-  float* s_q = s_p + cap;
-  float* s_u = s_q + cap;
-  int* s_tok = reinterpret_cast<int*>(s_u + cap);
+  double* s_p = reinterpret_cast<double*>(smem_raw + (VEC ? kVerifyRing : 0));
+  double* s_q = s_p + cap;
+  double* s_uq = s_q + cap;
+  int* s_tok = reinterpret_cast<int*>(s_uq + cap);
   int* s_par = s_tok + cap;
   int* s_gone = s_par + cap;
-  __shared__ double s_warp[kVerifyWarps], s_rank[2][8];
-  __shared__ uint64_t s_bar[kVerifyWarps][kVerifyStages];
+  // two sets of the cluster's warps' sums, used in turns: a warp sends its part of a
+  // sum only when it has read the one before, so a set is read by all before it is
+  // written again
+  __shared__ double s_warp[kVerifyWarps], s_piece[2][8 * kVerifyWarps];
+  __shared__ uint64_t s_bar[kVerifyWarps][kVerifyStages], s_sum_bar[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int s = blockIdx.x / ranks;
 
@@ -491,6 +592,16 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     for (int i = 0; i < kVerifyStages; ++i) mbar_init(smem_u32(&s_bar[warp][i]), 1);
     fence_barrier_init();
   }
+  const int pieces = ranks * kVerifyWarps;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&s_sum_bar[i]), 1);
+      mbar_arrive_expect_tx(smem_u32(&s_sum_bar[i]), pieces * 8);
+    }
+    fence_barrier_init();
+  }
+  // (no CTA writes into another's shared memory before that has set its barriers up)
+  auto others = cluster.barrier_arrive();
   pdl_wait();
   pdl_launch_dependents();
   const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
@@ -506,6 +617,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
       for (int i = tid; i < p.max_query_len; i += kVerifyThreads) out_tokens[i] = out_path[i] = -1;
       if (tid == 0) p.out_len[s] = 0;
     }
+    cluster.barrier_wait(std::move(others));
     return;
   }
   for (int i = 1 + tid; i < n; i += kVerifyThreads) {
@@ -518,60 +630,63 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     if (!(tok_ok && par_ok)) par = -1;  // never tried
     s_par[i] = par;
     s_tok[i] = tok;
-    s_u[i] = __ldg(p.u_accept + row);
-    s_p[i] = par >= 0 ? __ldg(p.target + (q0 + par) * p.target_stride + tok) : 0.0f;
-    s_q[i] = par >= 0 && p.draft != nullptr ? __ldg(p.draft + (q0 + par) * p.draft_stride + tok) : 1.0f;
+    // values not > 0 count as 0 (fmaxf: NaN too)
+    const float pt = par >= 0 ? fmaxf(__ldg(p.target + (q0 + par) * p.target_stride + tok), 0.0f) : 0.0f;
+    const float qt = par < 0 ? 0.0f : p.draft == nullptr ? 1.0f
+                     : fmaxf(__ldg(p.draft + (q0 + par) * p.draft_stride + tok), 0.0f);
+    s_p[i] = pt;
+    s_q[i] = qt;
+    s_uq[i] = static_cast<double>(__ldg(p.u_accept + row)) * static_cast<double>(qt);
   }
-  cluster.sync();  // (every CTA runs before any writes into another's shared memory)
+  cluster.barrier_wait(std::move(others));
+  __syncthreads();
 
   // this warp's piece of the vocabulary: whole groups of 128 values
-  const int pieces = ranks * kVerifyWarps;
   const int groups = (p.vocab + 127) / 128, per = (groups + pieces - 1) / pieces;
   const int piece = rank * kVerifyWarps + warp;
   const int lo = static_cast<int>(min(static_cast<int64_t>(piece) * per * 128, static_cast<int64_t>(p.vocab)));
   const int hi = static_cast<int>(min(static_cast<int64_t>(piece + 1) * per * 128, static_cast<int64_t>(p.vocab)));
 
-  auto load4 = [&](const float* row, int i, float (&x)[4]) {
-    if (VEC && i + 3 < p.vocab) {
-      const float4 f = __ldg(reinterpret_cast<const float4*>(row + i));
-      x[0] = f.x;
-      x[1] = f.y;
-      x[2] = f.z;
-      x[3] = f.w;
-    } else {
+  auto load4 = [&](const float* row, int i, int end, float (&x)[4]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = i + e < p.vocab ? __ldg(row + i + e) : 0.0f;
-    }
+    for (int e = 0; e < 4; ++e) x[e] = i + e < end ? __ldg(row + i + e) : 0.0f;
   };
-  // p and q of kVerifyBatch groups of 4 values of row `cur`: lane's own of the 128
-  // from i0 on, of the next 128, ... (0 from `end` on); all loads first
-  auto load_batch = [&](int cur, const Residual& r, int i0, int end, float (&x)[kVerifyBatch][4],
-                        float (&y)[kVerifyBatch][4]) {
-    const float* prow = p.target + (q0 + cur) * p.target_stride;
-    const float* qrow = p.draft + (q0 + cur) * p.draft_stride;
+  // values of one row: a lane's own of the 128 from i0 on, of the next 128, ... (0 from
+  // `end` on). A whole chunk's loads stand without conditions: behind one, the move of
+  // each loaded value waits for it before the next load.
+  auto load_batch = [&](const float* row, int i0, int end, float (&x)[kVerifyBatch][4]) {
+    row += i0 + lane * 4;
+    if (i0 + kVerifyChunk <= end) {
 #pragma unroll
-    for (int u = 0; u < kVerifyBatch; ++u) {
-      const int i = i0 + u * 128 + lane * 4;
+      for (int u = 0; u < kVerifyBatch; ++u) {
+        if constexpr (VEC) {
+          const float4 f = __ldg(reinterpret_cast<const float4*>(row + u * 128));
+          x[u][0] = f.x;
+          x[u][1] = f.y;
+          x[u][2] = f.z;
+          x[u][3] = f.w;
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[u][e] = y[u][e] = 0.0f;
-      if (i < end) {
-        load4(prow, i, x[u]);
-        if (r.t != 0.0) load4(qrow, i, y[u]);
-      }
-    }
-  };
-  // the masses of values i .. i + 3, from their p and q
-  auto masses = [&](const Residual& r, int i, const float (&x)[4], const float (&y)[4], double (&m)[4]) {
-    if (r.t != 0.0) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const double d = fma(-r.t, static_cast<double>(fmaxf(y[e], 0.0f)), static_cast<double>(fmaxf(x[e], 0.0f)));
-        const int keep = ~(__double2hiint(d) >> 31);  // by its sign (no NaN can be here)
-        m[e] = __hiloint2double(__double2hiint(d) & keep, __double2loint(d) & keep);
+          for (int e = 0; e < 4; ++e) x[u][e] = __ldg(row + u * 128 + e);
+        }
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) m[e] = static_cast<double>(fmaxf(x[e], 0.0f));
+      for (int u = 0; u < kVerifyBatch; ++u) load4(row, u * 128, end - i0 - lane * 4, x[u]);
+    }
+  };
+  // the masses of values i .. i + 3 from their p and q: with sampled drafts unscaled
+  // and any not > 0 standing for 0, else scaled and >= 0. Sampled: q by shifts, p by
+  // the conversion instruction, so that both pipes carry a part.
+  auto masses = [&](auto sampled, const Residual& r, int i, const float (&x)[4], const float (&y)[4],
+                    double (&m)[4]) {
+    if constexpr (sampled.value) {
+      const double t = -r.t * kUnscale;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[e] = fma(t, scaled(fmaxf(y[e], 0.0f)), static_cast<double>(x[e]));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) m[e] = scaled(fmaxf(x[e], 0.0f));
       for (int g = 0; g < r.gone; ++g) {
         const int t = s_gone[g] - i;
 #pragma unroll
@@ -583,227 +698,251 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
   // This warp's ring: chunks arrive by bulk copies while earlier ones are summed (a
   // warp's own loads would hold too few bytes in flight: a pass of 128,256 values
   // took 24 us in one CTA of 512 threads). A chunk's use of the ring goes on from
-  // the last one's, over all sums.
+  // the last one's, over all sums. What a sum leaves in the ring is the last
+  // chunks of p and q that it took; another sum over the same piece at the same
+  // node starts with them, as they are, and fetches the others meanwhile.
   const uint32_t ring = smem_u32(smem_raw) + warp * kVerifyStages * kVerifyChunk * 8;
-  int ring_st = 0;
-  uint32_t ring_ph = 0;
-  auto fetch = [&](int cur, const Residual& r, int i0, int end, int st) {
-    if (lane != 0) return;
+  [[maybe_unused]] int ring_st = 0;    // slot of the next chunk
+  [[maybe_unused]] uint32_t ring_ph = 0;  // a bit per slot: parity of its next arrival
+  [[maybe_unused]] int held = -1, held_at = 0;  // node whose chunks are in the ring; the last sum's first chunk
+  auto fetch = [&](int cur, bool both, int i0, int end, int st) {  // (by one lane)
     const uint32_t bytes = static_cast<uint32_t>(min(kVerifyChunk, end - i0) & ~3) * 4;
     const uint32_t bar = smem_u32(&s_bar[warp][st]), dst = ring + st * kVerifyChunk * 8;
-    const bool both = r.t != 0.0;
     mbar_arrive_expect_tx(bar, both ? 2 * bytes : bytes);
     if (bytes == 0) return;
     bulk_load(dst, p.target + (q0 + cur) * p.target_stride + i0, bytes, bar);
     if (both) bulk_load(dst + kVerifyChunk * 4, p.draft + (q0 + cur) * p.draft_stride + i0, bytes, bar);
   };
-  // a warp's sum over values [a, b)
-  auto sum_of = [&](int cur, const Residual& r, int a, int b) {
-    double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    if (VEC) {
-#pragma unroll
-      for (int k = 0; k < kVerifyStages; ++k)
-        if (a + k * kVerifyChunk < b) fetch(cur, r, a + k * kVerifyChunk, b, (ring_st + k) % kVerifyStages);
+  // a warp's sum over values [a, b); `whole`: they are its piece
+  auto sum_as = [&](auto sampled, int cur, const Residual& r, int a, int b, bool whole) {
+    double acc[kVerifyBatch][4] = {};
+    const int chunks = (b - a + kVerifyChunk - 1) / kVerifyChunk;
+    [[maybe_unused]] int at = 0, have = 0;  // first chunk taken; chunks in the ring already
+    if constexpr (VEC) {
+      if (whole && held == cur && chunks > 0) {
+        have = min(chunks, kVerifyStages);
+        at = held_at - have;
+        if (at < 0) at += chunks;
+        ring_st -= have;
+        if (ring_st < 0) ring_st += kVerifyStages;
+      }
+      if (lane >= have && lane < min(chunks, kVerifyStages))  // (a lane each: have is 0 or all)
+        fetch(cur, sampled.value, a + lane * kVerifyChunk, b, (ring_st + lane) % kVerifyStages);
+      held = whole && sampled.value ? cur : -1;
+      held_at = at;
     }
-    for (int i0 = a; i0 < b; i0 += kVerifyChunk) {
-      float x[kVerifyBatch][4], y[kVerifyBatch][4];
+    for (int k = 0, c = at; k < chunks; ++k) {
+      const int i0 = a + c * kVerifyChunk;
+      float x[kVerifyBatch][4] = {}, y[kVerifyBatch][4] = {};
       if constexpr (VEC) {
-        mbar_wait(smem_u32(&s_bar[warp][ring_st]), ring_ph, p.err);
+        if (k >= have) {
+          mbar_wait(smem_u32(&s_bar[warp][ring_st]), (ring_ph >> ring_st) & 1, p.err);
+          ring_ph ^= 1u << ring_st;
+        }
         const uint32_t src = ring + ring_st * kVerifyChunk * 8 + lane * 16;
+        if (i0 + kVerifyChunk <= b) {
+#pragma unroll
+          for (int u = 0; u < kVerifyBatch; ++u) {
+            ElemTraits<float>::unpack(lds128(src + u * 512), x[u]);
+            if (sampled.value) ElemTraits<float>::unpack(lds128(src + kVerifyChunk * 4 + u * 512), y[u]);
+          }
+        } else
 #pragma unroll
         for (int u = 0; u < kVerifyBatch; ++u) {
           const int i = i0 + u * 128 + lane * 4;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[u][e] = y[u][e] = 0.0f;
           if (i + 4 <= b) {
-            const uint4 px = lds128(src + u * 512);
-            ElemTraits<float>::unpack(px, x[u]);
-            if (r.t != 0.0) ElemTraits<float>::unpack(lds128(src + kVerifyChunk * 4 + u * 512), y[u]);
+            ElemTraits<float>::unpack(lds128(src + u * 512), x[u]);
+            if (sampled.value) ElemTraits<float>::unpack(lds128(src + kVerifyChunk * 4 + u * 512), y[u]);
           } else if (i < b) {  // the vocabulary's last one to three values
-            load4(p.target + (q0 + cur) * p.target_stride, i, x[u]);
-            if (r.t != 0.0) load4(p.draft + (q0 + cur) * p.draft_stride, i, y[u]);
+            load4(p.target + (q0 + cur) * p.target_stride, i, b, x[u]);
+            if (sampled.value) load4(p.draft + (q0 + cur) * p.draft_stride, i, b, y[u]);
           }
         }
       } else {
-        load_batch(cur, r, i0, b, x, y);
+        load_batch(p.target + (q0 + cur) * p.target_stride, i0, b, x);
+        if (sampled.value) load_batch(p.draft + (q0 + cur) * p.draft_stride, i0, b, y);
       }
 #pragma unroll
       for (int u = 0; u < kVerifyBatch; ++u) {
         double m[4];
-        masses(r, i0 + u * 128 + lane * 4, x[u], y[u], m);
+        masses(sampled, r, i0 + u * 128 + lane * 4, x[u], y[u], m);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[e] += m[e];
-      }
-      if constexpr (VEC) {
-        __syncwarp();  // every lane has read the chunk
-        if (i0 + kVerifyStages * kVerifyChunk < b)
-          fetch(cur, r, i0 + kVerifyStages * kVerifyChunk, b, ring_st);
-        if (++ring_st == kVerifyStages) {
-          ring_st = 0;
-          ring_ph ^= 1;
+        for (int e = 0; e < 4; ++e) {
+          if (sampled.value)
+            add_positive(acc[u][e], m[e]);
+          else
+            acc[u][e] += m[e];
         }
       }
+      if (++c == chunks) c = 0;
+      if constexpr (VEC) {
+        __syncwarp();  // every lane has read the chunk
+        if (lane == 0 && k + kVerifyStages < chunks) {
+          int f = at + k + kVerifyStages;
+          if (f >= chunks) f -= chunks;
+          fetch(cur, sampled.value, a + f * kVerifyChunk, b, ring_st);
+        }
+        if (++ring_st == kVerifyStages) ring_st = 0;
+      }
     }
-    double t = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    double t = 0.0;
+#pragma unroll
+    for (int u = 0; u < kVerifyBatch; ++u) t += (acc[u][0] + acc[u][1]) + (acc[u][2] + acc[u][3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFullMask, t, o);
-    return t;
+    return sampled.value ? t : t * kUnscale;
   };
   int turn = 0;
-  // the sum over the vocabulary; s_warp then holds the pieces' sums of this
-  // CTA and s_rank[which] the CTAs'
-  auto total_mass = [&](int cur, const Residual& r, int* which) {
-    const double acc = sum_of(cur, r, lo, hi);
-    __syncthreads();  // (earlier readers of s_warp are done)
-    if (lane == 0) s_warp[warp] = acc;
-    __syncthreads();
-    *which = turn;
-    if (warp == 0) {
-      double t = 0.0;
-      for (int w = 0; w < kVerifyWarps; ++w) t += s_warp[w];
-      if (lane < ranks) *cluster.map_shared_rank(&s_rank[turn][rank], lane) = t;
+  uint32_t turn_ph = 0;  // a bit per set of sums
+  // the sum over the vocabulary: every warp sends its piece's to every CTA;
+  // a lane then holds those of kVerifyPart pieces
+  auto total_mass = [&](double acc, double (&part)[kVerifyPart]) {
+    const uint32_t bar = smem_u32(&s_sum_bar[turn]);
+    if (lane < ranks)
+      store_async(cluster_address(smem_u32(&s_piece[turn][piece]), lane), acc, cluster_address(bar, lane));
+    mbar_wait_cluster(bar, (turn_ph >> turn) & 1, p.err);
+    turn_ph ^= 1u << turn;
+    if (tid == 0) mbar_arrive_expect_tx(bar, pieces * 8);  // for its next use
+#pragma unroll
+    for (int e = 0; e < kVerifyPart; ++e) {
+      const int at = kVerifyPart * lane + e;
+      part[e] = at < pieces ? s_piece[turn][at] : 0.0;
     }
-    cluster.sync();
+    turn ^= 1;
     double z = 0.0;
-    for (int c = 0; c < ranks; ++c) z += s_rank[turn][c];
-    turn ^= 1;  // (the next sum's writes to this slot lie behind another cluster.sync)
+#pragma unroll
+    for (int e = 0; e < kVerifyPart; ++e) z += part[e];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(kFullMask, z, o);
     return z;
   };
 
-  int cur = 0, len = 1, which = 0;
+  int cur = 0, len = 1;
   Residual r{0.0, 0};
-  double z = 1.0;
+  double z = 1.0, part[kVerifyPart];
   bool stale = false;  // z has not been summed since the last rejection
   if (rank == 0 && tid == 0) out_path[0] = 0;
-  for (int i = 1; i < n; ++i) {
-    if (s_par[i] != cur) continue;
-    if (stale) {
-      z = total_mass(cur, r, &which);
-      stale = false;
-    }
-    double left = mass_of(s_p[i], s_q[i], r.t);
-    for (int g = 0; g < r.gone; ++g)
-      if (s_gone[g] == s_tok[i]) left = 0.0;
-    const double qx = s_q[i] > 0.0f ? static_cast<double>(s_q[i]) : 0.0;
-    if (static_cast<double>(s_u[i]) * qx * z < left) {
-      if (rank == 0 && tid == 0) {
-        out_tokens[len - 1] = s_tok[i];
-        out_path[len] = i;
+  double want = 0.0, run = 0.0;  // of the search: the sum to pass, the sum before [a, b)
+  bool good = false;
+  // where the running sum passes `want` (by rounding, or with u outside [0, 1),
+  // nowhere: the last place with a mass)
+  auto narrow = [&](const Passed& f) {
+    run = f.first >= 0 ? f.first_before : f.last_before;
+    return f.first >= 0 ? f.first : f.last;
+  };
+  // which warp has it, given every warp's sum of its part
+  auto place = [&](double sum) {
+    __syncthreads();
+    if (lane == 0) s_warp[warp] = sum;
+    __syncthreads();
+    const double w[1] = {lane < kVerifyWarps ? s_warp[lane] : 0.0};
+    return narrow(find_passed(w, want, run, lane));
+  };
+  // The walk, each sum that it needs, and the search in a long piece go through one
+  // loop: the summing code then stands in the program once (in six places it was
+  // larger than the instruction cache likes).
+  int a = lo, b = hi, step = 0;  // step > 0: searching, a part of that many values a warp
+  bool mine = false;             // the place is in this CTA's piece [a, b)
+  for (int i = 1;;) {
+    if (step == 0) {
+      // on to the next child that needs a sum, or to the last row's
+      for (;; ++i) {
+        // the next row whose parent is `cur`
+        unsigned kin = 0;
+        for (int base = i & ~31; base < n; base += 32) {
+          const int row = base + lane;
+          kin = __ballot_sync(kFullMask, row >= i && row < n && s_par[row] == cur);
+          if (kin != 0) {
+            i = base + __ffs(kin) - 1;
+            break;
+          }
+        }
+        if (kin == 0) i = n;
+        if (i == n || stale) break;
+        double left = fmax(fma(-r.t, s_q[i], s_p[i]), 0.0);
+        for (int g = 0; g < r.gone; ++g)
+          if (s_gone[g] == s_tok[i]) left = 0.0;
+        if (s_uq[i] * z < left) {
+          if (rank == 0 && tid == 0) {
+            out_tokens[len - 1] = s_tok[i];
+            out_path[len] = i;
+          }
+          cur = i;
+          ++len;
+          r = Residual{0.0, 0};
+          z = 1.0;
+        } else if (p.draft != nullptr) {
+          r.t += z;
+          stale = true;
+        } else {
+          z = fmax(z - left, 0.0);
+          __syncthreads();
+          if (tid == 0) s_gone[r.gone] = s_tok[i];
+          __syncthreads();
+          ++r.gone;
+        }
       }
-      cur = i;
-      ++len;
-      r = Residual{0.0, 0};
-      z = 1.0;
-      continue;
     }
-    if (p.draft != nullptr) {
-      r.t += z;
-      stale = true;
+    const int from = step == 0 ? a : min(a + warp * step, b);
+    const int to = step == 0 ? b : min(from + step, b);
+    const double sum = r.t != 0.0 ? sum_as(std::true_type{}, cur, r, from, to, step == 0)
+                                  : sum_as(std::false_type{}, cur, r, from, to, step == 0);
+    if (step == 0) {
+      z = total_mass(sum, part);
+      if (i < n) {
+        stale = false;
+        continue;
+      }
+      if (!(z > 0.0) && (r.t != 0.0 || r.gone != 0)) {  // nothing left: the target's own row
+        r = Residual{0.0, 0};
+        continue;
+      }
+      // the lowest index whose running sum exceeds u z: its piece, then its place there
+      good = z > 0.0 && z < 0x1p127;  // (an infinite value counts 2^128)
+      if (!good) break;
+      want = static_cast<double>(__ldg(p.u_sample + s)) * z;
+      const int at = narrow(find_passed(part, want, run, lane));
+      mine = at / kVerifyWarps == rank;
+      if (!mine) break;
+      a = static_cast<int>(min(static_cast<int64_t>(at) * per * 128, static_cast<int64_t>(p.vocab)));
+      b = static_cast<int>(min(static_cast<int64_t>(at + 1) * per * 128, static_cast<int64_t>(p.vocab)));
     } else {
-      z = fmax(z - left, 0.0);
-      __syncthreads();
-      if (tid == 0) s_gone[r.gone] = s_tok[i];
-      __syncthreads();
-      ++r.gone;
+      a = min(a + place(sum) * step, b);
+      b = min(a + step, b);
     }
+    if (b - a <= kVerifyWarps * kVerifyChunk) break;
+    step = ((b - a + 127) / 128 + kVerifyWarps - 1) / kVerifyWarps * 128;
   }
-  z = total_mass(cur, r, &which);
-  if (!(z > 0.0)) {  // nothing left: the target's own row
-    r = Residual{0.0, 0};
-    z = total_mass(cur, r, &which);
-  }
-  // the lowest index whose running sum exceeds u z: its CTA, its warp's piece, its place
-  const bool good = z > 0.0 && z < INFINITY;
-  const double want = static_cast<double>(__ldg(p.u_sample + s)) * z;
-  int chosen = -1;
-  {
-    double before = 0.0;
-    int at = -1, last = -1;
-    double at_before = 0.0, last_before = 0.0;
-    for (int c = 0; c < ranks; ++c) {
-      const double t = s_rank[which][c];
-      if (t > 0.0) {
-        last = c;
-        last_before = before;
-      }
-      if (at < 0 && before + t > want) {
-        at = c;
-        at_before = before;
-      }
-      before += t;
-    }
-    if (at < 0) {  // rounding, or u outside [0, 1)
-      at = last;
-      at_before = last_before;
-    }
-    if (good && rank == at) {
-      // the first place of n whose running sum passes `want` (else the last with
-      // a sum), and the sum before it
-      auto place = [&](const double* sums, int n, double& run) {
-        double b2 = run, first_before = 0.0, last_before = 0.0;
-        int first = -1, end = -1;
-        for (int w = 0; w < n; ++w) {
-          const double t = sums[w];
-          if (t > 0.0) {
-            end = w;
-            last_before = b2;
-          }
-          if (first < 0 && b2 + t > want) {
-            first = w;
-            first_before = b2;
-          }
-          b2 += t;
-        }
-        run = first >= 0 ? first_before : last_before;
-        return first >= 0 ? first : end;
-      };
-      double run = at_before;
-      int w = place(s_warp, kVerifyWarps, run);
-      int a = min((rank * kVerifyWarps + w) * per * 128, p.vocab);
-      int b = min(a + per * 128, p.vocab);
-      if (per > kVerifyBatch) {
-        // a long piece: the CTA's warps sum a part each, and one of them has it
-        const int step = (per + kVerifyWarps - 1) / kVerifyWarps * 128;
-        const int sub = min(a + warp * step, b);
-        const double t = sum_of(cur, r, sub, min(sub + step, b));
-        __syncthreads();
-        if (lane == 0) s_warp[warp] = t;
-        __syncthreads();
-        w = place(s_warp, kVerifyWarps, run);
-        a = min(a + w * step, b);
-        b = min(a + step, b);
-      }
-      if (warp == w) {
-        int last_pos = -1;
-        for (int i0 = a; i0 < b && chosen < 0; i0 += kVerifyChunk) {
-          float x[kVerifyBatch][4], y[kVerifyBatch][4];
-          load_batch(cur, r, i0, b, x, y);
+  if (mine) {
+    // a chunk each: the warp that has it holds its values
+    float x[kVerifyBatch][4], y[kVerifyBatch][4] = {};
+    double m[kVerifyBatch][4], sum = 0.0;
+    const int i0 = a + warp * kVerifyChunk;
+    load_batch(p.target + (q0 + cur) * p.target_stride, i0, b, x);
+    if (r.t != 0.0) load_batch(p.draft + (q0 + cur) * p.draft_stride, i0, b, y);
 #pragma unroll
-          for (int u = 0; u < kVerifyBatch; ++u) {
-            const int i = i0 + u * 128 + lane * 4;
-            double m[4];
-            masses(r, i, x[u], y[u], m);
-            const double c0 = m[0], c1 = c0 + m[1], c2 = c1 + m[2], c3 = c2 + m[3];
-            double incl = c3;
+    for (int u = 0; u < kVerifyBatch; ++u) {
+      if (r.t != 0.0)
+        masses(std::true_type{}, r, i0 + u * 128 + lane * 4, x[u], y[u], m[u]);
+      else
+        masses(std::false_type{}, r, i0 + u * 128 + lane * 4, x[u], y[u], m[u]);
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const double t = __shfl_up_sync(kFullMask, incl, o);
-              if (lane >= o) incl += t;
-            }
-            const double bb = run + (incl - c3);
-            const int hit = m[0] > 0.0 && bb + c0 > want ? 0 : m[1] > 0.0 && bb + c1 > want ? 1
-                            : m[2] > 0.0 && bb + c2 > want ? 2 : m[3] > 0.0 && bb + c3 > want ? 3 : 4;
-            const int lastp = m[3] > 0.0 ? 3 : m[2] > 0.0 ? 2 : m[1] > 0.0 ? 1 : m[0] > 0.0 ? 0 : -1;
-            const unsigned hits = __ballot_sync(kFullMask, hit < 4);
-            const unsigned pos = __ballot_sync(kFullMask, lastp >= 0);
-            if (chosen < 0 && hits) chosen = __shfl_sync(kFullMask, i + hit, __ffs(hits) - 1);
-            if (pos) last_pos = __shfl_sync(kFullMask, i + lastp, 31 - __clz(pos));
-            run += __shfl_sync(kFullMask, incl, 31);
-          }
-        }
-        if (chosen < 0) chosen = last_pos;
-        if (lane == 0) out_tokens[len - 1] = chosen;
+      for (int e = 0; e < 4; ++e) {
+        m[u][e] = m[u][e] > 0.0 ? r.t != 0.0 ? m[u][e] : m[u][e] * kUnscale : 0.0;
+        sum += m[u][e];
       }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFullMask, sum, o);
+    if (warp == place(sum)) {
+      int chosen = -1, last = -1;
+#pragma unroll
+      for (int u = 0; u < kVerifyBatch; ++u) {
+        const Passed f = find_passed(m[u], want, run, lane);
+        if (chosen < 0 && f.first >= 0) chosen = i0 + u * 128 + f.first;
+        if (f.last >= 0) last = i0 + u * 128 + f.last;
+      }
+      if (lane == 0) out_tokens[len - 1] = chosen >= 0 ? chosen : last;
     }
   }
   if (rank == 0) {
@@ -814,7 +953,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const V
     for (int i = len + tid; i < p.max_query_len; i += kVerifyThreads) out_tokens[i] = out_path[i] = -1;
     if (tid == 0) p.out_len[s] = len;
   }
-  cluster.sync();  // no CTA leaves while another may still write its shared memory
+  // (a CTA may leave: all that others write into its shared memory has been waited for)
 }
 
 }  // namespace
@@ -842,20 +981,24 @@ cudaError_t launch_verify_draft(const VerifyShape& sh, int32_t* out_tokens, int3
   p.max_query_len = sh.max_query_len;
   cudaError_t e = device_error_word(&p.err);
   if (e != cudaSuccess) return e;
-  // CTAs per sequence: as many (up to the portable 8) as keep the launch within
-  // one wave of resident CTAs (two an SM) and leave each a few thousand values
-  // (128,256 values, one draw a sequence: 64 sequences 13.3 us with 4 CTAs, 20.4
-  // with 8; 256 sequences 36 with 1, 52 with 4; one sequence 9.4 with 8, 25.8 with 1)
+  // CTAs per sequence, up to the portable 8, each with a few thousand values at least.
+  // Where rows are summed again after rejections (trees with draft probabilities), 8: a
+  // sequence's sums follow each other, and 8 CTAs keep 3/4 of 128,256 values in their
+  // rings (7 rejections in each of 64 sequences: 44 us, with 4 CTAs 56; 64 trees of 16:
+  // 33.5 and 34.6). Else as many as keep the launch within one wave of resident CTAs, two an
+  // SM (one draw a sequence over 128,256 values: 64 sequences 10.2 us with 4 CTAs, 15.3 with
+  // 8; 256 sequences 28 us with 1, 53 with 8).
   int ranks = 1;
-  while (ranks < 8 && sh.num_seqs * ranks <= 148 && sh.vocab / ranks > 4096) ranks *= 2;
+  const bool again = draft != nullptr && parents != nullptr;
+  while (ranks < 8 && (again || sh.num_seqs * ranks <= 148) && sh.vocab / ranks > 4096) ranks *= 2;
   auto vec_ok = [](const float* x, int64_t stride) {
     return (reinterpret_cast<uintptr_t>(x) & 15) == 0 && stride % 4 == 0;
   };
   const bool vec = vec_ok(target, sh.target_stride) && (draft == nullptr || vec_ok(draft, sh.draft_stride));
   auto kernel = vec ? verify_draft_kernel<true> : verify_draft_kernel<false>;
-  const int smem = (vec ? kVerifyRing : 0) + sh.max_query_len * 24;
+  const int smem = (vec ? kVerifyRing : 0) + sh.max_query_len * 36;
   static std::atomic<unsigned long long> configured[2] = {{0}, {0}};
-  if ((e = ensure_smem(kernel, kVerifyRing + kMaxVerifyRows * 24, configured[vec])) != cudaSuccess) return e;
+  if ((e = ensure_smem(kernel, kVerifyRing + kMaxVerifyRows * 36, configured[vec])) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(sh.num_seqs) * ranks);
   cfg.blockDim = dim3(kVerifyThreads);
