@@ -656,11 +656,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       if (whole) {
         const float inv = 1.0f / l_run;
         if (relay) {
-          if (relay && failed) {  // let the other warp go
-      asm volatile("bar.arrive %0, 64;" ::"r"(wq >= 2 ? taken : there) : "memory");
-    } else if (left_some) {
-      asm volatile("bar.sync %0, 64;" ::"r"(taken) : "memory");
-    }
+          if (left_some) asm volatile("bar.sync %0, 64;" ::"r"(taken) : "memory");
           left_some = true;
           const uint32_t row_at = place + lane * D * 2;
           const int sw = (lane & 7) << 4;
@@ -733,7 +729,11 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       // published, which these threads do after the loads above)
       return true;
     });
-    if (left_some) asm volatile("bar.sync %0, 64;" ::"r"(taken) : "memory");
+    if (relay && failed) {  // let the other warp go
+      asm volatile("bar.arrive %0, 64;" ::"r"(wq >= 2 ? taken : there) : "memory");
+    } else if (left_some) {
+      asm volatile("bar.sync %0, 64;" ::"r"(taken) : "memory");
+    }
   }
 
   tc::fence_before_sync();
