@@ -222,3 +222,14 @@ def test_truncate_refuses_and_changes_nothing(new_len):
     with pytest.raises(pa.PagedAttentionError):
         bm.truncate(s + 1, 0)
     assert bm.seq_len(s) == 5 and bm.seq_num_blocks(s) == 2
+
+
+@pytest.mark.parametrize("call,args", [
+    (pa.pa_kv_accept, 7), (pa.pa_verify_draft, 10), (pa.pa_decode_tree, 11), (pa.pa_qk_norm_rope_append, 9),
+])
+def test_tensors_off_the_gpu_and_other_objects_are_refused(call, args):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        call(*[torch.zeros(2, 8, 1, 64)] * args)
+    with pytest.raises(TypeError, match="must be a tensor"):
+        call(*[3] * args)

@@ -127,6 +127,24 @@ def test_verify_matches_the_walk(counts, vocab, kind, sampled):
             assert all(np.array_equal(x, y) for x, y in zip(got, again))
 
 
+@pytest.mark.parametrize("vocab,pad", [(128256, 0), (130001, 3), (99001, 1)])
+def test_rows_summed_again_after_many_rejections(vocab, pad):
+    # more values than a cluster keeps on chip; (130001, 3): 16-byte-aligned rows with an odd end
+    b = draw_batch(vocab, [9, 12, 1, 10], vocab, "star", True, sharp=1.5, noise=0.7)
+    start = b["start"]
+    b["ua"][:] = 0.99999994
+    for s in (0, 1):                       # the least likely tokens: rejected
+        rows = slice(start[s] + 1, start[s + 1])
+        b["tokens"][rows] = np.argsort(b["target"][start[s]])[:start[s + 1] - start[s] - 1]
+    # the second one's sixth child is accepted, and its own children rejected again
+    six = start[1] + 6
+    b["tokens"][six], b["ua"][six] = int(b["target"][start[1]].argmax()), 0.0
+    b["parents"][six + 1:start[2]] = 6
+    b["tokens"][six + 1:start[2]] = np.argsort(b["target"][six])[:start[2] - six - 1]
+    check(b, run(b, pad=pad))
+    assert pa.pa_device_errors() == 0
+
+
 def test_rows_of_a_wider_tensor_and_wider_outputs():
     b = draw_batch(5, [6, 3], 1001, "tree", True)
     for pad in (1, 3, 23):
