@@ -36,6 +36,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -216,7 +217,11 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   using Cfg = TreeConfig<D, QT>;
   constexpr int NK = Cfg::kNK, NV = Cfg::kNV, NG = Cfg::kNG, KEYN = kTreeKeys, HALVES = Cfg::kHalves;
   extern __shared__ __align__(1024) uint8_t sm[];
-  const int pipe = Cfg::kPipes == 1 ? 0 : static_cast<int>(threadIdx.x) / Cfg::kPipeThreads;
+  // (the warp by a shuffle, so that the compiler knows it, and what the issuing warps derive
+  // from it, to be uniform: an MMA's operands then stay in uniform registers. Moved there
+  // for each, an MMA of 64 keys took 80 to 110 clocks to issue that runs in 48.)
+  const int cta_warp = __shfl_sync(kFullMask, static_cast<int>(threadIdx.x) >> 5, 0);
+  const int pipe = Cfg::kPipes == 1 ? 0 : cta_warp / (Cfg::kPipeThreads / 32);
   const int tid = static_cast<int>(threadIdx.x) - pipe * Cfg::kPipeThreads;  // of the pipeline
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + Cfg::kBars) + pipe * Cfg::kNumBars;
   auto bar = [&](int i) { return smem_u32(bars + i); };
@@ -232,8 +237,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   auto q_s = [&](int x) { return pipe_s + x * Cfg::kQBytes; };
   auto gran = [&](int st) { return pipe_s + Cfg::kRing + st * Cfg::kGran; };
 
-  const int warp = tid >> 5, lane = threadIdx.x & 31;  // (warp of the pipeline)
-  const int cta_warp = threadIdx.x >> 5;
+  const int warp = cta_warp - pipe * (Cfg::kPipeThreads / 32), lane = threadIdx.x & 31;  // (warp of the pipeline)
   const int G = 1 << p.lg_group, TOK = kTreeRows >> p.lg_group;
   const int item_tokens = QT * TOK;
   const int bs = p.block_size, lg = p.log2_block_size;
@@ -397,6 +401,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     // -------------------------------------------------------- S = Q K^T MMAs
     fewer();
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(kTreeRows, KEYN, 0);
+    const bool one = tc::elect_one();
     RingPos<NK> pos(0);
     uint32_t qph = 0;
     int it = 0;  // tiles so far, over all runs
@@ -412,7 +417,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
             if (!wait_all(bar(kO + 2 * x + (it & 1)), ((it - 2) >> 1) & 1)) return false;
         if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
         tc::fence_after_sync();
-        if (lane == 0) {
+        if (one) {
           // (a k-step's operands lie a constant on: added to the descriptor, in 16 bytes)
           const uint64_t kd = tc::smem_desc_sw128(gran(pos.st), 16, 1024);
 #pragma unroll
@@ -450,6 +455,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
     // ------------------------------------------------------------ P V MMAs
     fewer();
     constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
+    const bool one = tc::elect_one();
     RingPos<NV> pos(NK);
     int it = 0;
     runs([&](const TreeRun& r) {
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         for (int x = 0; x < QT; ++x) {
           if (!wait_all(bar(kP + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
           tc::fence_after_sync();
-          if (lane == 0) {
+          if (one) {
 #pragma unroll
             for (int ks = 0; ks < KEYN / 16; ++ks)
               tc::mma_bf16_tmem_a(t_o(x), t_s(x, it & 1) + ks * 8, vd + ((ks * 2048) >> 4), kIdPV,
@@ -468,7 +474,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
           }
           __syncwarp();
         }
-        if (lane == 0) tc::commit(bar(kEmpty + pos.st));
+        if (one) tc::commit(bar(kEmpty + pos.st));
         __syncwarp();
         pos.step();
       }
@@ -744,7 +750,7 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
 // Merge of the items that were split:
 //   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j
 // over all parts j. An item's pieces (32 rows x 4 columns, a lane one row) are
-// dealt to as many CTAs as it has parts. With fewer pieces than warps, W warps
+// dealt to as many CTAs as it has parts, times one per 64 rows. With fewer pieces than warps, W warps
 // share a piece, taking the parts in turn and joining in shared memory in their
 // order; so the sums' order goes by the item's rows and parts alone.
 // Latency-bound: a header, one round trip per kMergeParts W parts.
@@ -759,16 +765,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
   const int slot = blockIdx.x, cta = slot >> 1;
   const TreeHeader hd = p.hdr[slot];
   if (hd.first < 0) return;
-  const int rank = cta - hd.first, parts = hd.last - hd.first + 1;
+  const int parts = hd.last - hd.first + 1;
+  const int rank = (cta - hd.first) * gridDim.y + blockIdx.y, ctas = parts * gridDim.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (hd.rows + 31) >> 5, pieces = groups * (D / 4);
-  const int mine = (pieces - rank + parts - 1) / parts;  // pieces rank, rank + parts, ...
+  const int mine = (pieces - rank + ctas - 1) / ctas;  // pieces rank, rank + ctas, ...
   if (mine <= 0) return;
   const int W = mine >= 5 ? 1 : mine >= 3 ? 2 : mine == 2 ? 4 : 8;
   const int sub = warp & (W - 1);
   for (int k0 = 0; k0 < mine; k0 += kMergeWarps / W) {
     const int k = k0 + warp / W;
-    const int w = rank + k * parts;
+    const int w = rank + k * ctas;
     const int row = (w % groups) * 32 + lane, col = w / groups;
     const bool on = k < mine && row < hd.rows;
     float M = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -890,7 +897,10 @@ cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* 
   e = launch_pdl(pa_tree_kernel<D, QT>, dim3(parts / Cfg::kPipes), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
                  qmap, kmap, vmap, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(tree_merge_kernel<D>, dim3(2 * parts), dim3(kMergeWarps * 32), 0, stream, p);
+  // (an item's merge per 64 rows: two sequences of 8,192 tokens, items of 256 rows, 40.5 us
+  // with one CTA for each part, 34.7 with four)
+  return launch_pdl(tree_merge_kernel<D>, dim3(2 * parts, std::max(1, p.slot_rows / 64)), dim3(kMergeWarps * 32), 0,
+                    stream, p);
 }
 
 }  // namespace
