@@ -28,7 +28,8 @@
 //  * warp 0 / warp 1 (producers): K (and Q) / V tiles by TMA, boxes of {64
 //    columns, min(block_size, 64) tokens} with the 128-byte swizzle, into a
 //    ring of 64-key tiles each, running ahead across items.
-//  * warp 2: S_x = Q_x K^T (M 128, N 64), two tiles ahead; warp 3: O_x += P_x V.
+//  * warps 2, 3: S_x = Q_x K^T (M 128, N 64), two tiles ahead, and O_x += P_x V: one each, or
+//    (QT = 2) a query tile each.
 //  * 4 QT softmax warps, thread = row: as in the prefill kernel (base-2
 //    exponentials against a reference that moves when exceeded by 2^8, P in
 //    tensor memory over its S). P is rounded to bf16 (the type of V), and the row
@@ -252,10 +253,10 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < NG; ++i) {
       mbar_init(bar(kFull + i), 1);
-      mbar_init(bar(kEmpty + i), 1);
+      mbar_init(bar(kEmpty + i), QT);  // (two query tiles have an issuer each)
     }
     mbar_init(bar(kQFull), 1);
-    mbar_init(bar(kQEmpty), 1);
+    mbar_init(bar(kQEmpty), QT);
     for (int i = 0; i < 2 * QT; ++i) {
       mbar_init(bar(kS + i), 1);
       mbar_init(bar(kP + i), 128);
@@ -397,89 +398,107 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       }
       return true;
     });
-  } else if (warp == 2) {
-    // -------------------------------------------------------- S = Q K^T MMAs
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------- MMAs
     fewer();
     constexpr uint32_t kIdS = tc::idesc_bf16_f32(kTreeRows, KEYN, 0);
+    constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
     const bool one = tc::elect_one();
-    RingPos<NK> pos(0);
+    RingPos<NK> kpos(0);
+    RingPos<NV> vpos(NK);
+    // S of tile it (over all runs), of query tile x; false: a wait gave up
+    auto scores = [&](int x, int it) {
+      // this buffer of S held P of tile it - 2 until its P V was done
+      if (it >= 2 && !wait_all(bar(kO + 2 * x + (it & 1)), ((it - 2) >> 1) & 1)) return false;
+      if (!wait_all(bar(kFull + kpos.st), kpos.ph)) return false;
+      tc::fence_after_sync();
+      if (one) {
+        // (a k-step's operands lie a constant on: added to the descriptor, in 16 bytes)
+        const uint64_t kd = tc::smem_desc_sw128(gran(kpos.st), 16, 1024);
+        const uint64_t qd = tc::smem_desc_sw128(q_s(x), 16, 1024);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          tc::mma_bf16(t_s(x, it & 1), qd + (((ks >> 2) * Cfg::kQHalf + (ks & 3) * 32) >> 4),
+                       kd + (((ks >> 2) * Cfg::kGranHalf + (ks & 3) * 32) >> 4), kIdS, ks > 0);
+        tc::commit(bar(kS + 2 * x + (it & 1)));
+        tc::commit(bar(kEmpty + kpos.st));
+      }
+      __syncwarp();
+      kpos.step();
+      return true;
+    };
+    // O += P V of tile it, the run's first or not
+    auto outputs = [&](int x, int it, bool first) {
+      if (!wait_all(bar(kFull + vpos.st), vpos.ph)) return false;
+      if (!wait_all(bar(kP + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
+      tc::fence_after_sync();
+      if (one) {
+        const uint64_t vd = tc::smem_desc_sw128(gran(vpos.st), Cfg::kGranHalf, 1024);
+#pragma unroll
+        for (int ks = 0; ks < KEYN / 16; ++ks)
+          tc::mma_bf16_tmem_a(t_o(x), t_s(x, it & 1) + ks * 8, vd + ((ks * 2048) >> 4), kIdPV, !first || ks > 0);
+        tc::commit(bar(kO + 2 * x + (it & 1)));
+        tc::commit(bar(kEmpty + vpos.st));
+      }
+      __syncwarp();
+      vpos.step();
+      return true;
+    };
     uint32_t qph = 0;
     int it = 0;  // tiles so far, over all runs
     bool ended = false;
-    runs([&](const TreeRun& r) {
-      ended = false;
-      if (!wait_all(bar(kQFull), qph)) return false;
-      qph ^= 1;
-      for (int t = r.t0; t < r.t1; ++t, ++it) {
-        // this buffer of S held P of tile it - 2 until its P V was done
-        if (it >= 2)
-          for (int x = 0; x < QT; ++x)
-            if (!wait_all(bar(kO + 2 * x + (it & 1)), ((it - 2) >> 1) & 1)) return false;
-        if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
-        tc::fence_after_sync();
-        if (one) {
-          // (a k-step's operands lie a constant on: added to the descriptor, in 16 bytes)
-          const uint64_t kd = tc::smem_desc_sw128(gran(pos.st), 16, 1024);
-#pragma unroll
-          for (int x = 0; x < QT; ++x) {
-            const uint64_t qd = tc::smem_desc_sw128(q_s(x), 16, 1024);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-              tc::mma_bf16(t_s(x, it & 1), qd + (((ks >> 2) * Cfg::kQHalf + (ks & 3) * 32) >> 4),
-                           kd + (((ks >> 2) * Cfg::kGranHalf + (ks & 3) * 32) >> 4), kIdS, ks > 0);
-            tc::commit(bar(kS + 2 * x + (it & 1)));
+    if (QT == 2) {
+      // warp 2 + x: all of query tile x, S two tiles ahead of P V, so that neither query tile
+      // waits for the other's barriers (one warp for S and one for P V of both: four
+      // sequences of 32,768 tokens with 64 rows of 4 heads 151 us, this 147).
+      const int x = warp - 2;
+      runs([&](const TreeRun& r) {
+        ended = false;
+        if (!wait_all(bar(kQFull), qph)) return false;
+        qph ^= 1;
+        const int tiles = r.t1 - r.t0;
+        for (int t = 0; t < tiles + 2; ++t) {
+          if (t >= 2 && !outputs(x, it + t - 2, t == 2)) return false;
+          if (t < tiles) {
+            if (!scores(x, it + t)) return false;
+            if (t == tiles - 1 && one) tc::commit(bar(kQEmpty));
           }
-          tc::commit(bar(kEmpty + pos.st));
-          if (t == r.t1 - 1) tc::commit(bar(kQEmpty));
         }
-        __syncwarp();
-        pos.step();
-      }
-      ended = true;
-      return true;
-    });
+        it += tiles;
+        ended = true;
+        return true;
+      });
+    } else if (warp == 2) {
+      runs([&](const TreeRun& r) {
+        ended = false;
+        if (!wait_all(bar(kQFull), qph)) return false;
+        qph ^= 1;
+        for (int t = r.t0; t < r.t1; ++t, ++it)
+          if (!scores(0, it)) return false;
+        if (one) tc::commit(bar(kQEmpty));
+        ended = true;
+        return true;
+      });
+    } else {
+      runs([&](const TreeRun& r) {
+        for (int t = r.t0; t < r.t1; ++t, ++it)
+          if (!outputs(0, it, t == r.t0)) return false;
+        return true;
+      });
+    }
     // The CTA must not leave while a commit is still to arrive on its barriers.
     // The last phases of "S full" and "P V done" are waited for by their readers;
     // the last of each K and V place's and of Q's "empty" have no reader left, so
     // they are waited for here.
-    if (ended && lane < NG) {
-      const int n = lane < NK ? NK : NV, at = lane < NK ? lane : lane - NK;
-      const int uses = (it - at + n - 1) / n;  // of this lane's place
-      if (it > at) mbar_wait(bar(kEmpty + lane), (uses - 1) & 1, p.err);
-    }
-    if (ended) {
-      mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
-      __syncwarp();
-    }
-  } else if (warp == 3) {
-    // ------------------------------------------------------------ P V MMAs
-    fewer();
-    constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTreeRows, D, 1);
-    const bool one = tc::elect_one();
-    RingPos<NV> pos(NK);
-    int it = 0;
-    runs([&](const TreeRun& r) {
-      for (int t = r.t0; t < r.t1; ++t, ++it) {
-        if (!wait_all(bar(kFull + pos.st), pos.ph)) return false;
-        const uint64_t vd = tc::smem_desc_sw128(gran(pos.st), Cfg::kGranHalf, 1024);
-        for (int x = 0; x < QT; ++x) {
-          if (!wait_all(bar(kP + 2 * x + (it & 1)), (it >> 1) & 1)) return false;
-          tc::fence_after_sync();
-          if (one) {
-#pragma unroll
-            for (int ks = 0; ks < KEYN / 16; ++ks)
-              tc::mma_bf16_tmem_a(t_o(x), t_s(x, it & 1) + ks * 8, vd + ((ks * 2048) >> 4), kIdPV,
-                                  t > r.t0 || ks > 0);
-            tc::commit(bar(kO + 2 * x + (it & 1)));
-          }
-          __syncwarp();
-        }
-        if (one) tc::commit(bar(kEmpty + pos.st));
-        __syncwarp();
-        pos.step();
+    if (warp == 2 && ended) {
+      if (lane < NG) {
+        const int n = lane < NK ? NK : NV, at = lane < NK ? lane : lane - NK;
+        const int uses = (it - at + n - 1) / n;  // of this lane's place
+        if (it > at) mbar_wait(bar(kEmpty + lane), (uses - 1) & 1, p.err);
       }
-      return true;
-    });
+      mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
+    }
+    __syncwarp();
   } else {
     // -------------------------------------------------------------- softmax
     if constexpr (QT == 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
@@ -602,9 +621,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
           tc::st32(t_s(x, it & 1) + lane_off, pw);
           tc::wait_st();
         }
-        if (x == 0 && key0 + KEYN > r.L) {
+        if (key0 + KEYN > r.L) {
           // keys past the context: stale or unwritten V rows become zeros (their
-          // P is 0, but 0 * NaN would not be)
+          // P is 0, but 0 * NaN would not be), by each query tile for its own P V
           if (!wait_all(bar(kFull + vpos.st), vpos.ph)) return fail();
           const int nkeys = r.L - key0;
           const uint32_t vb = gran(vpos.st);
@@ -621,11 +640,10 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
         vpos.step();
         tc::fence_before_sync();
         mbar_arrive(bar(kP + 2 * x + (it & 1)));
-        if (t > r.t0 && !rescale) {
-          if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return fail();
-        }
       }
-      // the run's end: O of all its tiles
+      // the run's end: O of all its tiles. (A phase of "P V done" that is waited for is the
+      // next one of its barrier: S of tile i is issued after P V of tile i - 2.)
+      if (r.t1 - r.t0 > 1 && !wait_all(bar(kO + 2 * x + (it & 1)), ((it - 2) >> 1) & 1)) return fail();
       if (!wait_all(bar(kO + 2 * x + ((it - 1) & 1)), ((it - 1) >> 1) & 1)) return fail();
       tc::fence_after_sync();
       const bool whole = r.t0 == 0 && r.t1 == r.nt;
