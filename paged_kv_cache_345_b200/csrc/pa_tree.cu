@@ -914,7 +914,10 @@ cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* 
   const unsigned parts = static_cast<unsigned>(tree_pipelines(QT));
   e = launch_pdl(pa_tree_kernel<D, QT>, dim3(parts / Cfg::kPipes), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
                  qmap, kmap, vmap, p);
-  if (e != cudaSuccess) return e;
+  // Where no table holds an item long enough to be cut there is nothing to merge (one request
+  // of 300 tokens: 11.6 us with the empty launch, 10.2 without).
+  const int64_t tiles = (static_cast<int64_t>(sh.max_blocks_per_seq) * sh.block_size + kTreeKeys - 1) / kTreeKeys;
+  if (e != cudaSuccess || tiles + kTreeItemCost <= kTreeWhole) return e;
   // (an item's merge per 64 rows: two sequences of 8,192 tokens, items of 256 rows, 40.5 us
   // with one CTA for each part, 34.7 with four)
   return launch_pdl(tree_merge_kernel<D>, dim3(2 * parts, std::max(1, p.slot_rows / 64)), dim3(kMergeWarps * 32), 0,

@@ -158,6 +158,15 @@ def test_tree_matches_float64_on_drawn_batches(seed):
     check(b, b.run(), f"seed {seed}")
 
 
+@pytest.mark.parametrize("length", [383, 384, 385, 448, 449])
+@pytest.mark.parametrize("rows", [9, 70])
+def test_tables_around_the_shortest_that_may_be_cut(length, rows):
+    # (six tiles are not cut and need no merge; two sequences, so that a cut could fall inside)
+    for bs in (16, 64):
+        b = Batch([length - rows, 0], [rows, 1], 32, 8, 128, bs, "tree", seed=length + rows)
+        check(b, b.run(), f"block size {bs}")
+
+
 def test_more_sequences_than_threads():
     rng = np.random.default_rng(3)
     s = 700
