@@ -51,8 +51,11 @@ struct RowsParams {
 // and written once), if the instructions stay few: with the weights folded into
 // the cosines and sines once per unit,
 //   out[e] = r (x[e] cw[e] + z[e] sw[e]),  r = 1 / sqrt(mean(x^2) + eps),
-// z[e] the other element of the pair (its lane's 16 bytes are shuffled, not its
-// floats), all two elements to an instruction.
+// z[e] the other element of the pair, all two elements to an instruction. A lane
+// holds both elements of its pairs: its 16 bytes are 8 at the pairs' first
+// elements and 8 at their second ones (interleaved pairs: 16 in a row), so that
+// nothing is exchanged and a cosine or sine is loaded once (with 16 bytes in a row and the
+// partner's shuffled 10,578 prompt rows took 52.5 us, issuing 58 % of the time; _).
 template <typename T, int D>
 struct RowsConfig {
   static constexpr int kEPL = ElemTraits<T>::kPer16B;
@@ -102,7 +105,8 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
   const unsigned tok = unit / p.units_per_token;
   if (tok >= static_cast<unsigned>(p.num_tokens)) return;
   const int part = static_cast<int>(unit - tok * p.units_per_token);
-  const int lane = threadIdx.x & 31, li = lane % LPR, e0 = li * EPL;
+  constexpr int CH = EPL / 2;  // elements of 8 bytes
+  const int lane = threadIdx.x & 31, li = lane % LPR;
   const int pos = __ldg(p.positions + tok);
   const int64_t slot = __ldg(p.slots + tok);
   // kind 0 q, 1 k, 2 v (the same for the warp), and its heads
@@ -111,14 +115,27 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
   const int head0 = (part - (kind == 0 ? 0 : kind == 1 ? p.q_units : p.q_units + p.kv_units)) * Cfg::kPer +
                     lane / LPR;
   const T* src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                 tok * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + head0 * D + e0;
+                 tok * (kind == 0 ? p.q_stride : kind == 1 ? p.k_stride : p.v_stride) + head0 * D;
+  // this lane's elements: ea .. ea + CH - 1 and eb .. eb + CH - 1
+  const int half = p.rotary_dim >> 1;
+  const bool rotated = INTERLEAVED ? li * EPL < p.rotary_dim : li * CH < half;
+  const int ea = INTERLEAVED ? li * EPL : rotated ? li * CH : p.rotary_dim + (li * CH - half) * 2;
+  const int eb = INTERLEAVED || !rotated ? ea + CH : ea + half;
   uint4 raw[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     raw[u] = make_uint4(0, 0, 0, 0);
     // (not the read-only path: q_out may be q)
-    if (head0 + u * Cfg::kRows < heads)
-      raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + u * Cfg::kRows * D));
+    if (head0 + u * Cfg::kRows < heads) {
+      const T* row = src + u * Cfg::kRows * D;
+      if constexpr (INTERLEAVED) {
+        raw[u] = __ldcs(reinterpret_cast<const uint4*>(row + ea));
+      } else {
+        const uint2 a = __ldcs(reinterpret_cast<const uint2*>(row + ea));
+        const uint2 b = __ldcs(reinterpret_cast<const uint2*>(row + eb));
+        raw[u] = make_uint4(a.x, a.y, b.x, b.y);
+      }
+    }
   }
   if (pos < 0) return;  // padding
   if (pos >= p.max_position) {
@@ -129,29 +146,26 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
   if (kind != 0 && (slot < 0 || slot >= p.num_slots)) return;
   uint8_t* cache = static_cast<uint8_t*>(kind == 1 ? p.k_cache : p.v_cache);
   const int64_t cache_row = slot * p.num_kv_heads + head0;
-  T* dst = kind == 0 ? static_cast<T*>(p.q_out) + tok * p.q_out_stride + head0 * D + e0
-                     : reinterpret_cast<T*>(cache) + cache_row * D + e0;
+  T* dst = kind == 0 ? static_cast<T*>(p.q_out) + tok * p.q_out_stride + head0 * D
+                     : reinterpret_cast<T*>(cache) + cache_row * D;
 
+  // pairs of elements (2 i, 2 i + 1) of the lane's; the other element of a pair is the
+  // neighbour (interleaved), or in the lane's other 8 bytes
   uint64_t cw[NP], sw[NP];
-  int partner = lane;  // lane that holds the other elements of this lane's pairs
-  const int half = p.rotary_dim >> 1;
-  const bool rotated = e0 < p.rotary_dim;
   const T* weight = static_cast<const T*>(kind == 0 ? p.q_weight : p.k_weight);
   if (kind < 2) {
-    float c[EPL], n[EPL], w[EPL], wp[EPL];
+    float c[EPL], n[EPL];
     if (rotated) {
-      constexpr int NC = INTERLEAVED ? NP : EPL;
-      float cs[NC], sn[NC];
-      const float* t = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim +
-                       (INTERLEAVED ? e0 / 2 : e0 < half ? e0 : e0 - half);
-      load_floats<NC>(t, cs);
-      load_floats<NC>(t + half, sn);
-      if (!INTERLEAVED) partner = e0 < half ? lane + half / EPL : lane - half / EPL;
+      float cs[CH], sn[CH];
+      const float* t = p.cos_sin + static_cast<int64_t>(pos) * p.rotary_dim + (INTERLEAVED ? ea / 2 : ea);
+      load_floats<CH>(t, cs);
+      load_floats<CH>(t + half, sn);
 #pragma unroll
       for (int e = 0; e < EPL; ++e) {
-        c[e] = cs[INTERLEAVED ? e / 2 : e];
-        const bool first = INTERLEAVED ? e % 2 == 0 : e0 < half;
-        n[e] = first ? -sn[INTERLEAVED ? e / 2 : e] : sn[INTERLEAVED ? e / 2 : e];
+        const int angle = INTERLEAVED ? e / 2 : e % CH;
+        const bool first = INTERLEAVED ? e % 2 == 0 : e < CH;
+        c[e] = cs[angle];
+        n[e] = first ? -sn[angle] : sn[angle];
       }
     } else {
 #pragma unroll
@@ -161,17 +175,14 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
       }
     }
     if (weight != nullptr) {
-      ElemTraits<T>::unpack(__ldg(reinterpret_cast<const uint4*>(weight + e0)), w);
-      if (INTERLEAVED) {
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) wp[e] = w[e ^ 1];
-      } else {
-        ElemTraits<T>::unpack(__ldg(reinterpret_cast<const uint4*>(weight + (partner % LPR) * EPL)), wp);
-      }
+      const uint2 wa = __ldg(reinterpret_cast<const uint2*>(weight + ea));
+      const uint2 wb = __ldg(reinterpret_cast<const uint2*>(weight + eb));
+      float w[EPL];
+      ElemTraits<T>::unpack(make_uint4(wa.x, wa.y, wb.x, wb.y), w);
 #pragma unroll
       for (int e = 0; e < EPL; ++e) {
         c[e] *= w[e];
-        n[e] *= wp[e];
+        n[e] *= w[INTERLEAVED ? e ^ 1 : (e + CH) % EPL];
       }
     }
 #pragma unroll
@@ -187,26 +198,20 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
     const bool on = head0 + u * Cfg::kRows < heads;
     uint64_t y[NP];
     if (kind < 2) {
-      uint64_t x[NP], z[NP];
+      uint64_t x[NP];
       unpack_pairs<T>(raw[u], x);
-      if constexpr (INTERLEAVED) {
 #pragma unroll
-        for (int i = 0; i < NP; ++i) {
+      for (int i = 0; i < NP; ++i) {
+        uint64_t z = x[(i + NP / 2) % NP];
+        if constexpr (INTERLEAVED) {
           float lo, hi;
           floats_of(x[i], lo, hi);
-          z[i] = rotated ? pair_of(hi, lo) : 0;
+          z = pair_of(hi, lo);
         }
-      } else {
-        uint4 o;
-        o.x = __shfl_sync(kFullMask, raw[u].x, partner);
-        o.y = __shfl_sync(kFullMask, raw[u].y, partner);
-        o.z = __shfl_sync(kFullMask, raw[u].z, partner);
-        o.w = __shfl_sync(kFullMask, raw[u].w, partner);
-        if (!rotated) o = make_uint4(0, 0, 0, 0);  // (an infinite x is not a pair of itself)
-        unpack_pairs<T>(o, z);
+        y[i] = mul2(x[i], cw[i]);
+        // (elsewhere an infinite x is not a pair of itself)
+        if (rotated) y[i] = fma2(z, sw[i], y[i]);
       }
-#pragma unroll
-      for (int i = 0; i < NP; ++i) y[i] = fma2(z[i], sw[i], mul2(x[i], cw[i]));
       if (weight != nullptr) {
         uint64_t sq = mul2(x[0], x[0]);
 #pragma unroll
@@ -237,7 +242,13 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
         for (int i = 0; i < 2; ++i)
           r[i] = static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(f[4 * i], sc), __fdiv_rn(f[4 * i + 1], sc))) |
                  (static_cast<uint32_t>(f32x2_to_e4m3x2(__fdiv_rn(f[4 * i + 2], sc), __fdiv_rn(f[4 * i + 3], sc))) << 16);
-        *reinterpret_cast<uint2*>(cache + (cache_row + u * Cfg::kRows) * D + e0) = make_uint2(r[0], r[1]);
+        uint8_t* row = cache + (cache_row + u * Cfg::kRows) * D;
+        if constexpr (INTERLEAVED) {
+          *reinterpret_cast<uint2*>(row + ea) = make_uint2(r[0], r[1]);
+        } else {
+          *reinterpret_cast<uint32_t*>(row + ea) = r[0];
+          *reinterpret_cast<uint32_t*>(row + eb) = r[1];
+        }
       }
       continue;
     }
@@ -249,7 +260,13 @@ __global__ void __launch_bounds__(RowsConfig<T, D>::kWarps * 32)
       else
         o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
-    *reinterpret_cast<uint4*>(dst + u * Cfg::kRows * D) = o;
+    T* row = dst + u * Cfg::kRows * D;
+    if constexpr (INTERLEAVED) {
+      *reinterpret_cast<uint4*>(row + ea) = o;
+    } else {
+      *reinterpret_cast<uint2*>(row + ea) = make_uint2(o.x, o.y);
+      *reinterpret_cast<uint2*>(row + eb) = make_uint2(o.z, o.w);
+    }
   }
 }
 
