@@ -34,6 +34,11 @@
 //    exponentials against a reference that moves when exceeded by 2^8, P in
 //    tensor memory over its S). P is rounded to bf16 (the type of V), and the row
 //    sum adds the rounded weights, so that they sum to 1 exactly.
+//
+// Measured (32 query and 8 KV heads, head_dim 128, back to back, with the merge): 256
+// sequences of lognormal lengths (621 MB of K and V) with 1 to 16 rows each 120 us, 5.2
+// TB/s; 4 sequences of 32,768 tokens with 64 rows each 147 us, 930 TFLOP/s: there a tile
+// takes a pipeline 2,000 clocks, its exponentials 1,024 and its MMAs 1,244 of them.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
@@ -771,7 +776,8 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
 // dealt to as many CTAs as it has parts, times one per 64 rows. With fewer pieces than warps, W warps
 // share a piece, taking the parts in turn and joining in shared memory in their
 // order; so the sums' order goes by the item's rows and parts alone.
-// Latency-bound: a header, one round trip per kMergeParts W parts.
+// Latency-bound: a header, one round trip per kMergeParts W parts (12 us alone after 256
+// sequences, 14 after 4 with 64 rows; about 2 of them before it starts).
 constexpr int kMergeParts = 7, kMergeWarps = 8;
 
 template <int D>
