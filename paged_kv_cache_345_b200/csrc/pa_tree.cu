@@ -36,8 +36,8 @@
 //    sum adds the rounded weights, so that they sum to 1 exactly.
 //
 // Measured (32 query and 8 KV heads, head_dim 128, back to back, with the merge): 256
-// sequences of lognormal lengths (621 MB of K and V) with 1 to 16 rows each 120 us, 5.2
-// TB/s; 4 sequences of 32,768 tokens with 64 rows each 147 us, 930 TFLOP/s: there a tile
+// sequences of lognormal lengths (621 MB of K and V) with 1 to 16 rows each 116 us, 5.3
+// TB/s; 4 sequences of 32,768 tokens with 64 rows each 144 us, 950 TFLOP/s: there a tile
 // takes a pipeline 2,000 clocks, its exponentials 1,024 and its MMAs 1,244 of them.
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -772,18 +772,19 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
 
 // Merge of the items that were split:
 //   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j
-// over all parts j. An item's pieces (32 rows x 4 columns, a lane one row) are
-// dealt to as many CTAs as it has parts, times one per 64 rows. With fewer pieces than warps, W warps
-// share a piece, taking the parts in turn and joining in shared memory in their
-// order; so the sums' order goes by the item's rows and parts alone.
-// Latency-bound: a header, one round trip per kMergeParts W parts (12 us alone after 256
-// sequences, 14 after 4 with 64 rows; about 2 of them before it starts).
-constexpr int kMergeParts = 7, kMergeWarps = 8;
+// over all parts j. An item's pieces (32 rows x 4 kMergeCols columns, a lane one row)
+// are dealt to as many CTAs as it has parts, times one per 128 rows. With fewer pieces
+// than warps, W warps share a piece, taking the parts in turn and joining in shared
+// memory in their order; so the sums' order goes by the item's rows and parts alone.
+// Bound by the round trips of a warp, kMergeParts W parts each: with 16 columns a lane
+// (eight loads in flight; of 7 parts and 4 columns two were, most items having two parts)
+// the merge adds 4.4 us to 8 requests (7.3 before) and 5 to 256 (9).
+constexpr int kMergeParts = 2, kMergeCols = 4, kMergeWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 2) tree_merge_kernel(const TreeParams p) {
   __shared__ float s_m[kMergeWarps][32], s_l[kMergeWarps][32];
-  __shared__ float4 s_acc[kMergeWarps][32];
+  __shared__ float4 s_acc[kMergeWarps][kMergeCols][32];
   pdl_wait();
   pdl_launch_dependents();
   const int slot = blockIdx.x, cta = slot >> 1;
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
   const int parts = hd.last - hd.first + 1;
   const int rank = (cta - hd.first) * gridDim.y + blockIdx.y, ctas = parts * gridDim.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (hd.rows + 31) >> 5, pieces = groups * (D / 4);
+  const int groups = (hd.rows + 31) >> 5, pieces = groups * (D / 4 / kMergeCols);
   const int mine = (pieces - rank + ctas - 1) / ctas;  // pieces rank, rank + ctas, ...
   if (mine <= 0) return;
   const int W = mine >= 5 ? 1 : mine >= 3 ? 2 : mine == 2 ? 4 : 8;
@@ -800,15 +801,38 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
   for (int k0 = 0; k0 < mine; k0 += kMergeWarps / W) {
     const int k = k0 + warp / W;
     const int w = rank + k * ctas;
-    const int row = (w % groups) * 32 + lane, col = w / groups;
+    const int row = (w % groups) * 32 + lane, col = w / groups * kMergeCols;  // (columns in fours)
     const bool on = k < mine && row < hd.rows;
-    float M = -INFINITY, l = 0.0f, acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float M = -INFINITY, l = 0.0f;
+    float4 acc[kMergeCols];
+#pragma unroll
+    for (int c = 0; c < kMergeCols; ++c) acc[c] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto scale = [&](float f) {
+      l *= f;
+#pragma unroll
+      for (int c = 0; c < kMergeCols; ++c) {
+        acc[c].x *= f;
+        acc[c].y *= f;
+        acc[c].z *= f;
+        acc[c].w *= f;
+      }
+    };
+    auto add = [&](float f, float l2, const float4 (&v)[kMergeCols]) {
+      l = fmaf(f, l2, l);
+#pragma unroll
+      for (int c = 0; c < kMergeCols; ++c) {
+        acc[c].x = fmaf(f, v[c].x, acc[c].x);
+        acc[c].y = fmaf(f, v[c].y, acc[c].y);
+        acc[c].z = fmaf(f, v[c].z, acc[c].z);
+        acc[c].w = fmaf(f, v[c].w, acc[c].w);
+      }
+    };
     if (on) {
       const float* ml = reinterpret_cast<const float*>(p.ws_ml + row);
       const float* av = p.ws_acc + (static_cast<int64_t>(col) * p.slot_rows + row) * 4;
       for (int j0 = sub; j0 < parts; j0 += kMergeParts * W) {
         float2 mq[kMergeParts];
-        float4 v[kMergeParts];
+        float4 v[kMergeParts][kMergeCols];
 #pragma unroll
         for (int j = 0; j < kMergeParts; ++j) {
           const int jj = j0 + j * W;
@@ -817,27 +841,18 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
             // the first part lies in its pipeline's second slot, the others in the first
             const int64_t sl = 2 * static_cast<int64_t>(hd.first + jj) + (jj == 0 ? 1 : 0);
             mq[j] = ld_cg_f32x2(ml + sl * p.slot_rows * 2);
-            v[j] = ld_cg_f32x4(av + sl * p.slot_rows * D);
+#pragma unroll
+            for (int c = 0; c < kMergeCols; ++c) v[j][c] = ld_cg_f32x4(av + (sl * D + c * 4) * p.slot_rows);
           }
         }
         float bm = M;
 #pragma unroll
         for (int j = 0; j < kMergeParts; ++j) bm = fmaxf(bm, mq[j].x);
         if (bm == -INFINITY) continue;  // this row saw no key in these parts
-        const float sc = exp2f(M - bm);
-        l *= sc;
+        scale(exp2f(M - bm));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] *= sc;
-#pragma unroll
-        for (int j = 0; j < kMergeParts; ++j) {
-          if (mq[j].x == -INFINITY) continue;  // (no part, or none of its keys seen)
-          const float wt = exp2f(mq[j].x - bm);
-          l = fmaf(wt, mq[j].y, l);
-          acc[0] = fmaf(wt, v[j].x, acc[0]);
-          acc[1] = fmaf(wt, v[j].y, acc[1]);
-          acc[2] = fmaf(wt, v[j].z, acc[2]);
-          acc[3] = fmaf(wt, v[j].w, acc[3]);
-        }
+        for (int j = 0; j < kMergeParts; ++j)
+          if (mq[j].x != -INFINITY) add(exp2f(mq[j].x - bm), mq[j].y, v[j]);  // (else no part, or none of its keys seen)
         M = bm;
       }
     }
@@ -845,20 +860,19 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
       __syncthreads();
       s_m[warp][lane] = M;
       s_l[warp][lane] = l;
-      s_acc[warp][lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+#pragma unroll
+      for (int c = 0; c < kMergeCols; ++c) s_acc[warp][c][lane] = acc[c];
       __syncthreads();
       if (sub != 0) continue;
       for (int i = 1; i < W; ++i) {
         const float m2 = s_m[warp + i][lane];
         if (m2 == -INFINITY) continue;
         const float bm = fmaxf(M, m2);
-        const float f1 = exp2f(M - bm), f2 = exp2f(m2 - bm);
-        const float4 v = s_acc[warp + i][lane];
-        l = l * f1 + s_l[warp + i][lane] * f2;
-        acc[0] = acc[0] * f1 + v.x * f2;
-        acc[1] = acc[1] * f1 + v.y * f2;
-        acc[2] = acc[2] * f1 + v.z * f2;
-        acc[3] = acc[3] * f1 + v.w * f2;
+        float4 v[kMergeCols];
+#pragma unroll
+        for (int c = 0; c < kMergeCols; ++c) v[c] = s_acc[warp + i][c][lane];
+        scale(exp2f(M - bm));
+        add(exp2f(m2 - bm), s_l[warp + i][lane], v);
         M = bm;
       }
     }
@@ -866,8 +880,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 3) tree_merge_kernel(const T
     const float inv = 1.0f / l;
     const int64_t out = hd.out_row + static_cast<int64_t>(row >> p.lg_group) * p.num_heads +
                         (row & ((1 << p.lg_group) - 1));
-    *reinterpret_cast<uint2*>(p.out + out * D + col * 4) =
-        make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+    __nv_bfloat16* dst = p.out + out * D + col * 4;
+#pragma unroll
+    for (int c = 0; c < kMergeCols; ++c)
+      *reinterpret_cast<uint2*>(dst + 4 * c) =
+          make_uint2(pack_bf16x2(acc[c].x * inv, acc[c].y * inv), pack_bf16x2(acc[c].z * inv, acc[c].w * inv));
   }
 }
 
@@ -924,9 +941,9 @@ cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* 
   // of 300 tokens: 11.6 us with the empty launch, 10.2 without).
   const int64_t tiles = (static_cast<int64_t>(sh.max_blocks_per_seq) * sh.block_size + kTreeKeys - 1) / kTreeKeys;
   if (e != cudaSuccess || tiles + kTreeItemCost <= kTreeWhole) return e;
-  // (an item's merge per 64 rows: two sequences of 8,192 tokens, items of 256 rows, 40.5 us
-  // with one CTA for each part, 34.7 with four)
-  return launch_pdl(tree_merge_kernel<D>, dim3(2 * parts, std::max(1, p.slot_rows / 64)), dim3(kMergeWarps * 32), 0,
+  // (two CTAs for each part of an item of 256 rows; more only add CTAs, which cost more than
+  // they save: of smaller items 592 are launched, eight times as many took 7 us longer)
+  return launch_pdl(tree_merge_kernel<D>, dim3(2 * parts, std::max(1, p.slot_rows / 128)), dim3(kMergeWarps * 32), 0,
                     stream, p);
 }
 
