@@ -486,22 +486,28 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
       });
     } else {
       runs([&](const TreeRun& r) {
+        ended = false;
         for (int t = r.t0; t < r.t1; ++t, ++it)
           if (!outputs(0, it, t == r.t0)) return false;
+        ended = true;
         return true;
       });
     }
     // The CTA must not leave while a commit is still to arrive on its barriers.
     // The last phases of "S full" and "P V done" are waited for by their readers;
     // the last of each K and V place's and of Q's "empty" have no reader left, so
-    // they are waited for here.
-    if (warp == 2 && ended) {
-      if (lane < NG) {
+    // they are waited for here, by a warp that has taken the place's last tile: the
+    // tile was loaded after the phase before. (A warp that has not could find that
+    // phase still open, and the one before it, of the same parity, passed: two
+    // commits of a thread arrive in no order that is promised.)
+    if (ended) {
+      const bool mine = QT == 2 ? warp == 2 : (lane < NK) == (warp == 2);
+      if (lane < NG && mine) {
         const int n = lane < NK ? NK : NV, at = lane < NK ? lane : lane - NK;
         const int uses = (it - at + n - 1) / n;  // of this lane's place
         if (it > at) mbar_wait(bar(kEmpty + lane), (uses - 1) & 1, p.err);
       }
-      mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
+      if (warp == 2) mbar_wait(bar(kQEmpty), qph ^ 1, p.err);
     }
     __syncwarp();
   } else {
