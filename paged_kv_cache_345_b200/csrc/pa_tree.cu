@@ -778,7 +778,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
 
 // Merge of the items that were split:
 //   M = max m_j,  out = sum 2^(m_j - M) O_j / sum 2^(m_j - M) l_j
-// over all parts j. An item's pieces (32 rows x 4 kMergeCols columns, a lane one row)
+// over all parts j in which the row saw a key: those whose sum l_j is not 0. (Not by m_j:
+// it is -inf as well where all that the row saw are NaN, whose sum is NaN, and so is the
+// row then.) An item's pieces (32 rows x 4 kMergeCols columns, a lane one row)
 // are dealt to as many CTAs as it has parts, times one per 128 rows. With fewer pieces
 // than warps, W warps share a piece, taking the parts in turn and joining in shared
 // memory in their order; so the sums' order goes by the item's rows and parts alone.
@@ -852,13 +854,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) tree_merge_kernel(const T
           }
         }
         float bm = M;
+        bool any = false;
 #pragma unroll
-        for (int j = 0; j < kMergeParts; ++j) bm = fmaxf(bm, mq[j].x);
-        if (bm == -INFINITY) continue;  // this row saw no key in these parts
+        for (int j = 0; j < kMergeParts; ++j) {
+          bm = fmaxf(bm, mq[j].x);
+          any |= mq[j].y != 0.0f;
+        }
+        if (!any) continue;  // this row saw no key in these parts
         scale(exp2f(M - bm));
 #pragma unroll
         for (int j = 0; j < kMergeParts; ++j)
-          if (mq[j].x != -INFINITY) add(exp2f(mq[j].x - bm), mq[j].y, v[j]);  // (else no part, or none of its keys seen)
+          if (mq[j].y != 0.0f) add(exp2f(mq[j].x - bm), mq[j].y, v[j]);  // (else no part, or none of its keys seen)
         M = bm;
       }
     }
@@ -871,14 +877,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 2) tree_merge_kernel(const T
       __syncthreads();
       if (sub != 0) continue;
       for (int i = 1; i < W; ++i) {
-        const float m2 = s_m[warp + i][lane];
-        if (m2 == -INFINITY) continue;
+        const float m2 = s_m[warp + i][lane], l2 = s_l[warp + i][lane];
+        if (l2 == 0.0f) continue;
         const float bm = fmaxf(M, m2);
         float4 v[kMergeCols];
 #pragma unroll
         for (int c = 0; c < kMergeCols; ++c) v[c] = s_acc[warp + i][c][lane];
         scale(exp2f(M - bm));
-        add(exp2f(m2 - bm), s_l[warp + i][lane], v);
+        add(exp2f(m2 - bm), l2, v);
         M = bm;
       }
     }
