@@ -50,6 +50,8 @@ const char* type_name(at::ScalarType t) {
     case at::kBFloat16: return "torch.bfloat16";
     case at::kInt: return "torch.int32";
     case at::kLong: return "torch.int64";
+    case at::kByte: return "torch.uint8";
+    case at::kFloat8_e4m3fn: return "torch.float8_e4m3fn";
     default: return c10::toString(t);
   }
 }
@@ -157,7 +159,10 @@ struct Cache {
 Cache caches(Call& c, PyObject* ko, PyObject* vo) {
   const at::Tensor& k = c.tensor(ko, "k_cache");
   const pa_dtype type = cache_type(k);
-  const at::Tensor& v = c.tensor(vo, "v_cache", k.scalar_type());
+  // (E4M3 codes: uint8 and float8_e4m3fn are the same bytes, and K and V may differ in it)
+  const at::Tensor& v = c.tensor(vo, "v_cache");
+  if (v.scalar_type() != k.scalar_type() && !(is_codes(k.scalar_type()) && is_codes(v.scalar_type())))
+    raise(PyExc_TypeError, "v_cache must be %s, got %s", type_name(k.scalar_type()), type_name(v.scalar_type()));
   if (k.dim() != 4) raise(PyExc_ValueError, "k_cache must be [num_blocks, block_size, num_kv_heads, head_dim]");
   if (v.sizes() != k.sizes()) raise(PyExc_ValueError, "cache shape mismatch");
   return Cache{k, v, narrow(k.size(0), "num_blocks"), narrow(k.size(1), "block_size"),
@@ -204,6 +209,7 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Call c;
     const Cache kv = caches(c, a[3], a[4]);
     const at::ScalarType dt = kv.k.scalar_type();
+    c.tensor(a[4], "v_cache", dt);
     const at::Tensor& k = c.tensor(a[0], "k_new", dt);
     const at::Tensor& v = c.tensor(a[1], "v_new", dt);
     const at::Tensor& slots = c.tensor(a[2], "slot_mapping", at::kLong);
