@@ -705,7 +705,7 @@ int pa_verify_draft(int32_t* out_tokens, int32_t* out_path, int32_t* out_len,
  *                  step, as pa_verify_draft's out_path.
  *   path_len       device, int32 [num_seqs], in [0, min(n, max_path_len)].
  *   context_lens, query_start  as the step's pa_decode_tree.
- * Blocks that hold the step's rows must not be shared. A bad range sets
+ * Blocks that hold the step's rows must not be shared (pa_bm_unshare). A bad range sets
  * PA_DEVERR_CONTEXT, a bad path or length PA_DEVERR_DRAFT (the sequence is
  * skipped from its 32-entry stretch of the path on), a table entry outside the
  * pool PA_DEVERR_BLOCK_ID (that row is skipped). Any dtype; block_size a power
@@ -862,6 +862,20 @@ int pa_bm_block_tables(const pa_bm* bm, const int32_t* seq_ids, int n, int32_t* 
  * nothing changes then.
  */
 int pa_bm_truncate(pa_bm* bm, int32_t seq_id, int32_t new_len);
+
+/*
+ * pa_bm_unshare — make the blocks that hold the last counts[i] tokens of sequence
+ * seq_ids[i] its own, for i < n, in that order (ids distinct): each of them that
+ * another sequence holds too (a fork taken since the tokens were written) is
+ * replaced in this sequence's table by a fresh block, and the pair (old, fresh) is
+ * written to cow_pairs (host, int64 [cow_capacity][2]). The caller must run
+ * pa_copy_blocks on those pairs before it changes the tokens (pa_kv_accept).
+ * *num_cow receives the number of pairs. All or nothing: if the pool lacks the
+ * blocks, a count is outside [0, length], or cow_capacity is too small, returns
+ * PA_ERR_NO_BLOCKS / PA_ERR_INVALID and changes nothing.
+ */
+int pa_bm_unshare(pa_bm* bm, const int32_t* seq_ids, const int32_t* counts, int n,
+                  int64_t* cow_pairs, int cow_capacity, int* num_cow);
 
 #ifdef __cplusplus
 }

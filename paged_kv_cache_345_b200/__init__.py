@@ -149,6 +149,7 @@ _sig("pa_bm_seq_num_blocks", _i32, _vp, ctypes.c_int32)
 _sig("pa_bm_append_slots", _i32, _vp, _i32p, _i32p, _i32, _i64p, _i64p, _i32,
      ctypes.POINTER(ctypes.c_int))
 _sig("pa_bm_truncate", _i32, _vp, ctypes.c_int32, ctypes.c_int32)
+_sig("pa_bm_unshare", _i32, _vp, _i32p, _i32p, _i32, _i64p, _i32, ctypes.POINTER(ctypes.c_int))
 _sig("pa_bm_block_tables", _i32, _vp, _i32p, _i32, _i32p, _i32, _i32p)
 
 EXPORTED = (
@@ -160,6 +161,7 @@ EXPORTED = (
     "pa_prefill_plan", "pa_prefill_planned",
     "pa_qk_norm_rope_append", "pa_decode_tree", "pa_decode_tree_workspace_bytes",
     "pa_verify_draft", "pa_kv_accept", "pa_bm_truncate",
+    "pa_bm_unshare",
     "pa_prefill", "pa_decode_noalloc", "pa_decode_noalloc_scratch_bytes", "pa_device_errors",
     "pa_last_error", "pa_status_string", "pa_alloc_create",
     "pa_alloc_destroy", "pa_alloc_block", "pa_incref", "pa_decref", "pa_refcount", "pa_num_free",
@@ -905,6 +907,21 @@ class BlockManager:
     def truncate(self, seq: int, new_len: int) -> None:
         """Drop the sequence's tokens past new_len; blocks left empty lose its reference."""
         _check(_lib.pa_bm_truncate(self._h, seq, new_len))
+
+    def unshare(self, seq_ids, counts):
+        """Make the blocks of each sequence's last counts[i] tokens its own; returns
+        cow_pairs (int64 [k, 2]): blocks to copy before the tokens are changed."""
+        ids, pids = _i32_array(seq_ids)
+        cnt, pcnt = _i32_array(counts)
+        if ids.shape != cnt.shape:
+            raise ValueError("seq_ids and counts differ in length")
+        # (the blocks that n tokens lie in; a negative count is refused below)
+        room = int((np.maximum(cnt, 0) // self.block_size + 2).sum())
+        cows = np.empty((max(room, 1), 2), dtype=np.int64)
+        ncow = ctypes.c_int(0)
+        _check(_lib.pa_bm_unshare(self._h, pids, pcnt, ids.size, cows.ctypes.data_as(_i64p),
+                                  cows.shape[0], ctypes.byref(ncow)))
+        return cows[:ncow.value].copy()
 
     def append_slots(self, seq_ids, counts, slots_out=None, cows_out=None):
         """Reserve slots; returns (slot_mapping int64 [sum(counts)], cow_pairs int64 [k, 2]).

@@ -313,9 +313,13 @@ class PagedKVCache:
     def accept(self, seq_ids, counts, path, path_len):
         """Keep the rows that pa_verify_draft kept (its out_path and out_len) of the step of
         counts[i] rows per sequence; the others' slots go back. Returns the new context
-        lengths (waits for path_len)."""
+        lengths (waits for path_len). Blocks of the step's rows that a fork taken since
+        write_rows shares are copied first: the fork keeps all rows of the step."""
         if not len(seq_ids):
             return []
+        cows = self.bm.unshare(seq_ids, counts)
+        if len(cows):
+            pa_copy_blocks(self.k_cache, self.v_cache, self._to_device(cows), stream=self.stream)
         block_tables, context_lens, _ = self.tables(seq_ids)
         pa_kv_accept(self.k_cache, self.v_cache, block_tables, context_lens,
                      self._to_device(self._query_start(counts)), path, path_len,

@@ -346,6 +346,66 @@ int pa_bm_truncate(pa_bm* bm, int32_t seq_id, int32_t new_len) {
   return PA_OK;
 }
 
+int pa_bm_unshare(pa_bm* bm, const int32_t* seq_ids, const int32_t* counts, int n,
+                  int64_t* cow_pairs, int cow_capacity, int* num_cow) {
+  if (!bm || n < 0 || (n > 0 && (!seq_ids || !counts)) || !num_cow)
+    return pa_fail(PA_ERR_INVALID, "pa_bm_unshare: null or negative argument");
+  const int bs = bm->block_size;
+  // Counted as the loop below goes, before anything changes: of a block's holders in
+  // this batch the last keeps it.
+  int64_t need = 0;
+  std::unordered_map<int32_t, int32_t> dropped;
+  try {
+    std::vector<int32_t> sorted(seq_ids, seq_ids + n);
+    std::sort(sorted.begin(), sorted.end());
+    if (std::adjacent_find(sorted.begin(), sorted.end()) != sorted.end())
+      return pa_fail(PA_ERR_INVALID, "pa_bm_unshare: a sequence id appears twice");
+    for (int i = 0; i < n; ++i) {
+      const Seq* s = bm->get(seq_ids[i]);
+      if (!s) return pa_fail(PA_ERR_INVALID, "pa_bm_unshare: unknown sequence %d", seq_ids[i]);
+      if (counts[i] < 0 || counts[i] > s->length)
+        return pa_fail(PA_ERR_INVALID, "pa_bm_unshare: count %d outside [0, %lld]", counts[i],
+                       static_cast<long long>(s->length));
+      if (counts[i] == 0) continue;
+      for (size_t b = static_cast<size_t>((s->length - counts[i]) / bs); b < s->blocks.size(); ++b) {
+        const int32_t id = s->blocks[b];
+        if (bm->pool->refcount[id] == 1) continue;
+        int32_t& gone = dropped[id];
+        if (bm->pool->refcount[id] - gone > 1) {
+          gone += 1;
+          need += 1;
+        }
+      }
+    }
+  } catch (...) {
+    return pa_fail(PA_ERR_INVALID, "pa_bm_unshare: out of host memory");
+  }
+  if (need > cow_capacity || (need > 0 && !cow_pairs))
+    return pa_fail(PA_ERR_INVALID, "pa_bm_unshare: %lld copy-on-write pairs, capacity %d",
+                   static_cast<long long>(need), cow_capacity);
+  if (need > static_cast<int64_t>(bm->pool->free_stack.size()))
+    return pa_fail(PA_ERR_NO_BLOCKS, "pa_bm_unshare: need %lld blocks, %zu free",
+                   static_cast<long long>(need), bm->pool->free_stack.size());
+  int ncow = 0;
+  for (int i = 0; i < n; ++i) {
+    Seq& s = *bm->get(seq_ids[i]);
+    if (counts[i] == 0) continue;
+    for (size_t b = static_cast<size_t>((s.length - counts[i]) / bs); b < s.blocks.size(); ++b) {
+      const int32_t shared = s.blocks[b];
+      if (bm->pool->refcount[shared] == 1) continue;
+      int32_t fresh;
+      pa_alloc_block(bm->pool, &fresh);  // cannot fail: counted above
+      pa_decref(bm->pool, shared);
+      s.blocks[b] = fresh;
+      cow_pairs[2 * ncow] = shared;
+      cow_pairs[2 * ncow + 1] = fresh;
+      ++ncow;
+    }
+  }
+  *num_cow = ncow;
+  return PA_OK;
+}
+
 int pa_bm_block_tables(const pa_bm* bm, const int32_t* seq_ids, int n, int32_t* tables,
                        int max_blocks_per_seq, int32_t* context_lens) {
   if (!bm || n < 0 || (n > 0 && (!seq_ids || !tables)) || max_blocks_per_seq <= 0)
