@@ -274,16 +274,24 @@ class PagedKVCache:
                    k_weight=None, eps: float = 1e-6, interleaved: bool = False, q_out=None):
         """Append counts[i] rows to seq_ids[i] with their norms and rotation: q [N, Hq, d],
         k, v [N, Hkv, d] (parts of one packed projection will do), positions int32 [N]
-        and cos_sin on the device; the rotated queries are returned."""
+        and cos_sin on the device; the rotated queries are returned. A call that raises
+        leaves the sequences as long as they were."""
         slots, cows = self.bm.append_slots(seq_ids, counts)
-        if len(cows):
-            pa_copy_blocks(self.k_cache, self.v_cache, self._to_device(cows), stream=self.stream)
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
-        if len(slots):
-            sc = dict(k_scale=self.k_scale, v_scale=self.v_scale) if self.fp8 else {}
-            pa_qk_norm_rope_append(q_out, q, k, v, positions, self._to_device(slots), self.k_cache,
-                                   self.v_cache, cos_sin, q_weight, k_weight, eps, interleaved,
-                                   stream=self.stream, **sc)
+        try:
+            if len(cows):
+                pa_copy_blocks(self.k_cache, self.v_cache, self._to_device(cows),
+                               stream=self.stream)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if len(slots) or len(q):
+                sc = dict(k_scale=self.k_scale, v_scale=self.v_scale) if self.fp8 else {}
+                pa_qk_norm_rope_append(q_out, q, k, v, positions, self._to_device(slots),
+                                       self.k_cache, self.v_cache, cos_sin, q_weight, k_weight,
+                                       eps, interleaved, stream=self.stream, **sc)
+        except Exception:
+            for s, n in zip(seq_ids, counts):
+                self.bm.truncate(s, self.bm.seq_len(s) - int(n))
+            raise
         return q_out
 
     def _query_start(self, counts):
