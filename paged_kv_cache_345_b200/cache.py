@@ -329,11 +329,14 @@ class PagedKVCache:
         if len(cows):
             pa_copy_blocks(self.k_cache, self.v_cache, self._to_device(cows), stream=self.stream)
         block_tables, context_lens, _ = self.tables(seq_ids)
-        pa_kv_accept(self.k_cache, self.v_cache, block_tables, context_lens,
-                     self._to_device(self._query_start(counts)), path, path_len,
-                     stream=self.stream)
+        query_start = self._to_device(self._query_start(counts))
         kept = path_len.tolist()
-        lens = [self.bm.seq_len(s) - int(n) + int(k) for s, n, k in zip(seq_ids, counts, kept)]
+        for n, k in zip(counts, kept):
+            if not 0 <= k <= min(int(n), path.shape[1]):
+                raise ValueError(f"path_len {k} outside [0, {min(int(n), path.shape[1])}]")
+        pa_kv_accept(self.k_cache, self.v_cache, block_tables, context_lens, query_start, path,
+                     path_len, stream=self.stream)
+        lens = [self.bm.seq_len(s) - int(n) + k for s, n, k in zip(seq_ids, counts, kept)]
         for s, n in zip(seq_ids, lens):
             self.bm.truncate(s, n)
         return lens
