@@ -37,6 +37,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import sysconfig
 
 import numpy as np
 
@@ -271,8 +272,12 @@ def _native():
     functions of the library loaded above. Needs torch, so it is loaded at the first use."""
     global _native_module
     if _native_module is None:
-        _torch()
+        torch = _torch()
         from . import _pa_torch
+        here = f"{torch.__version__} {sysconfig.get_config_var('SOABI')}"
+        if _pa_torch.built_for != here:
+            raise ImportError(f"_pa_torch.so was built for torch {_pa_torch.built_for}, this is "
+                              f"{here}: run paged_kv_cache_345_b200/build.py")
         names = ("pa_kv_append", "pa_kv_append_fp8", "pa_qk_norm_rope_append", "pa_decode_tree",
                  "pa_verify_draft", "pa_kv_accept", "pa_last_error")
         _pa_torch.bind({n: ctypes.cast(getattr(_lib, n), ctypes.c_void_p).value for n in names},

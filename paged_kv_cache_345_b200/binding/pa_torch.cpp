@@ -419,4 +419,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_torch", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__pa_torch(void) { return PyModule_Create(&module); }
+// (built_for: the torch and Python that this was built for, which the package checks)
+PyMODINIT_FUNC PyInit__pa_torch(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "built_for", PA_BUILT_FOR) != 0) Py_CLEAR(m);
+  return m;
+}

@@ -5,7 +5,8 @@ Usage: python paged_kv_cache_345_b200/build.py [--force] [--verbose]
 (run it by path: importing the package first would load the library.)
 The shared libraries land next to this file; objects go to _build/ at the
 repository root. A rebuild happens only when a source or header is newer than
-the libraries (or with --force).
+the libraries, when the binding was built for another torch or Python than the
+installed ones, or with --force.
 """
 
 from __future__ import annotations
@@ -13,10 +14,12 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +29,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 BINDING = os.path.join(PKG, "binding", "pa_torch.cpp")
 BINDING_LIB = os.path.join(PKG, "_pa_torch.so")
+STAMP = os.path.join(BUILD, "pa_torch.built_for")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3,-Wall",
@@ -48,17 +52,27 @@ def _inputs():
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def built_for() -> str:
+    """What the binding depends on besides its source: the installed torch and Python."""
+    try:
+        torch_version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch_version = "none"
+    return f"torch {torch_version}, {sysconfig.get_config_var('SOABI')}"
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING_LIB):
+    if not all(os.path.exists(p) for p in (LIB, BINDING_LIB, STAMP)):
         return False
+    with open(STAMP) as f:
+        if f.read() != built_for():
+            return False
     t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING_LIB))
     return all(os.path.getmtime(p) <= t for p in [*_inputs(), BINDING])
 
 
 def _build_binding() -> None:
     """Compile the torch binding against the installed torch and Python headers."""
-    import sysconfig
-
     import torch
 
     base = os.path.dirname(os.path.abspath(torch.__file__))
@@ -66,6 +80,7 @@ def _build_binding() -> None:
     tmp = BINDING_LIB + ".tmp"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-Wno-unknown-pragmas", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DPA_BUILT_FOR="{torch.__version__} {sysconfig.get_config_var("SOABI")}"',
            "-I", INCLUDE, "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(base, "include"),
            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
@@ -75,6 +90,8 @@ def _build_binding() -> None:
     if res.returncode != 0:
         raise RuntimeError(f"{cmd[0]} failed on {os.path.basename(BINDING)}:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING_LIB)
+    with open(STAMP, "w") as f:
+        f.write(built_for())
 
 
 def _compile(src: str, verbose: bool) -> str:
