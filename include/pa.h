@@ -569,7 +569,12 @@ int pa_prefill_planned(void* out, const void* q, const void* k_cache, const void
  * and V are the last n of its context_lens[s] = L cached tokens: row i is in
  * cache position L - n + i, whatever its depth. parents (int32 [total_q]) names
  * the row that each follows, within its sequence: an earlier row, or -1 for a
- * row that follows the context alone. NULL: chains (row i follows row i - 1).
+ * row that follows the context alone. NULL: chains (row i follows row i - 1), which
+ * pa_decode_tree attends without walking from row to row: for chains of hundreds of
+ * rows, give NULL.
+ *
+ * The rows, their verification and the move of those kept take every cache type;
+ * their attention reads bfloat16 caches.
  */
 
 /*

@@ -27,11 +27,12 @@ workspace. Each method marshals arguments and calls libpa.so:
   the drafted ones, a chain or a tree):
   write_rows(q, k, v, seq_ids, counts, positions, cos_sin)  reserve the rows'
       slots (shared tail blocks copied first), then norm, rotate and write them
-      in one pass (pa_qk_norm_rope_append); returns the queries.
+      in one pass (pa_qk_norm_rope_append); returns the queries. Any cache type.
   decode_tree(q, seq_ids, counts, parents)  every row attends what was cached
       before the step, itself and its ancestors (pa_decode_tree); bf16.
   accept(seq_ids, counts, path, path_len)  after pa_verify_draft: move the kept
-      rows into place (pa_kv_accept) and give the others' slots back.
+      rows into place (pa_kv_accept; blocks that a fork shares are copied first)
+      and give the others' slots back. Any cache type.
 
 dtype "fp8_e4m3": the caches hold uint8 E4M3 codes with one float32 scale per
 KV head (k_scale, v_scale); rows come in as bfloat16 and are quantised on the

@@ -583,8 +583,14 @@ __device__ __forceinline__ void mbar_wait_cluster(uint32_t bar, uint32_t parity,
 // piece is then searched. All in float64. The bytes are one row of p and one of q per
 // sequence; what bounds it are the sums of a sequence, one after the other: each
 // needs the one before (about 2.4 us each over 128,256 values, of which the walk's and
-// the exchange's latency is a third). 64 trees of 16 over 128,256 values: 36.6 us;
-// one chain of 5 over 32,000: 6.8 us; 256 plain draws (p alone, 131 MB): 28 us.
+// the exchange's latency is a third). Over 128,256 values: 64 trees of 16 41 us (inputs
+// not in L2; 37 to 43 by the drawn numbers), 64 picked trees 30; 64 chains of 5 17.9, of 8
+// 18.5, 64 picked chains of 5 15.7; 256 chains of 5 52, picked 43, 256 plain draws (p alone,
+// 131 MB) 29. One chain of 5 over 32,000: 6.9 us.
+//
+// Rows that are not 16-byte aligned (VEC false: a vocabulary of 50,257, say) are read by
+// plain loads instead of the rings: bulk copies need the alignment. 64 trees of 16 over
+// 50,257 values 39.0 us, over 50,256 31.6; 64 picked chains of 5 10.9 and 10.9.
 template <bool VEC>
 __global__ void __launch_bounds__(kVerifyThreads, 2) verify_draft_kernel(const VerifyParams p) {
   namespace cg = cooperative_groups;

@@ -35,10 +35,12 @@
 //    tensor memory over its S). P is rounded to bf16 (the type of V), and the row
 //    sum adds the rounded weights, so that they sum to 1 exactly.
 //
-// Measured (32 query and 8 KV heads, head_dim 128, back to back, with the merge): 256
-// sequences of lognormal lengths (621 MB of K and V) with 1 to 16 rows each 116 us, 5.3
-// TB/s; 4 sequences of 32,768 tokens with 64 rows each 144 us, 950 TFLOP/s: there a tile
-// takes a pipeline 2,000 clocks, its exponentials 1,024 and its MMAs 1,244 of them.
+// Measured (32 query and 8 KV heads, head_dim 128, with the merge): 256 sequences of
+// lognormal lengths (621 MB of K and V) with 1 to 16 rows each 117 us, 5.3 TB/s; 4
+// sequences of 32,768 tokens with 64 rows each 144 us, 950 TFLOP/s: there a tile takes a
+// pipeline 2,000 clocks, its exponentials 1,024 and its MMAs 1,244 of them. That is a
+// dozen launches at 1,965 MHz; launched without a pause the SM clock falls to about 1,480
+// MHz under the power limit, and the same launches take 126 and 172 us (4.9 TB/s, 800 TFLOP/s).
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 
@@ -567,6 +569,9 @@ __global__ void __launch_bounds__(TreeConfig<D, QT>::kThreads, 1)
                 if (top >= 63) seen = ~0ull;
                 else if (top >= 0) seen |= (2ull << top) - 1;
               } else {
+                // (a load for each ancestor, one after the other, in each of the row's own
+                // tiles: 4 sequences of 8,192 tokens and a chain of 64 rows 52.6 us, of 512
+                // 538, of 2,048 14,150; without parents 51.0, 298 and 1,270)
                 int a = my_tok, up = parent;
                 while (a >= rel) {
                   if (a - rel < 64) seen |= 1ull << (a - rel);
@@ -949,8 +954,9 @@ cudaError_t launch_tree_t(const TreeShape& sh, const TreeParams& p, const void* 
   const unsigned parts = static_cast<unsigned>(tree_pipelines(QT));
   e = launch_pdl(pa_tree_kernel<D, QT>, dim3(parts / Cfg::kPipes), dim3(Cfg::kThreads), Cfg::kSmemBytes, stream,
                  qmap, kmap, vmap, p);
-  // Where no table holds an item long enough to be cut there is nothing to merge (one request
-  // of 300 tokens: 11.6 us with the empty launch, 10.2 without).
+  // Where no table holds an item long enough to be cut there is nothing to merge. The host
+  // knows the tables' width, not the lengths: one request of 300 tokens takes 10.0 us with a
+  // table of its length, and 11.7, with the empty launch, with one for 32,768 tokens.
   const int64_t tiles = (static_cast<int64_t>(sh.max_blocks_per_seq) * sh.block_size + kTreeKeys - 1) / kTreeKeys;
   if (e != cudaSuccess || tiles + kTreeItemCost <= kTreeWhole) return e;
   // (two CTAs for each part of an item of 256 rows; more only add CTAs, which cost more than
